@@ -1,0 +1,212 @@
+// Device-side building blocks of the matrix products: fragments of the 32x32 matrix
+// instructions, the epilogue, and the walk over experts' token segments.
+#pragma once
+
+#include "mxq_device.h"
+#include "mxq_mm_launch.h"
+
+namespace mxq {
+
+typedef int v4i __attribute__((ext_vector_type(4)));
+typedef int v8i __attribute__((ext_vector_type(8)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+
+// Codes of the f8f6f4 matrix instructions' format fields.
+constexpr int kE4M3 = 0, kE2M1 = 4;
+
+// ---------------------------------------------------------------------------
+// Fragments. A lane of a 32x32x64 instruction holds 32 elements of operand row
+// (lane % 32): with h = lane / 32, E2M1 elements [32h, 32h + 32) in 16 bytes, and E4M3
+// elements [16h, 16h + 16) and [32 + 16h, 48 + 16h) in 32 bytes (checked on the chip);
+// the scale byte of lane half h multiplies elements [32h, 32h + 32).
+// Result register i of a lane is row 8 (i / 4) + 4h + i % 4 of the first operand and
+// row (lane % 32) of the second. The weight goes first, so a lane holds runs of four
+// consecutive output columns of one output row.
+
+__device__ __forceinline__ v8i widen(v4i v) { return v8i{v[0], v[1], v[2], v[3], 0, 0, 0, 0}; }
+
+// Eight elements (a bf16 fragment of a 32x32x16 instruction) from E4M3 bytes or E2M1
+// codes, times the scale: exact, E4M3 and E2M1 significands have at most 4 bits.
+__device__ __forceinline__ bf16x8 bf16_from_e4m3(uint32_t lo, uint32_t hi, float scale) {
+  const bf16x2_t a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, scale, false);
+  const bf16x2_t b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, scale, true);
+  const bf16x2_t c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, scale, false);
+  const bf16x2_t d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, scale, true);
+  return bf16x8{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
+}
+__device__ __forceinline__ bf16x8 bf16_from_e2m1(uint32_t w, float scale) {
+  const bf16x2_t a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, scale, 0);
+  const bf16x2_t b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, scale, 1);
+  const bf16x2_t c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, scale, 2);
+  const bf16x2_t d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, scale, 3);
+  return bf16x8{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
+}
+
+// ---------------------------------------------------------------------------
+// Activations and their derivatives in fp32. exp and the reciprocal are the hardware's
+// (about 1e-7 relative).
+__device__ __forceinline__ float sigmoid_f(float z) {
+  return __builtin_amdgcn_rcpf(1.0f + __expf(-z));
+}
+constexpr float kGeluA = 1.5957691216057308f;          // 2 sqrt(2/pi)
+constexpr float kGeluB = 1.5957691216057308f * 0.044715f;
+// tanh(u) = 2 sigmoid(2u) - 1, so the tanh form of GELU is z sigmoid(2u).
+__device__ __forceinline__ float gelu_f(float z) { return z * sigmoid_f(z * fmaf(kGeluB * z, z, kGeluA)); }
+
+__device__ __forceinline__ float act_f(float z, int act) {
+  switch (act) {
+    case kActRelu: return z < 0.0f ? 0.0f : z;
+    case kActGelu: return gelu_f(z);
+    case kActSilu: return z * sigmoid_f(z);
+  }
+  return z;
+}
+
+// ---------------------------------------------------------------------------
+// Epilogue of V consecutive columns [n0, n0 + V) of one row: bias, z, activation,
+// residual. V is 4 or 8 and n0 a multiple of V. Rows are `vec` when every row of d, z
+// and the residual starts on a V-element boundary (n % V == 0), else element by element.
+template <typename T>
+struct Out;
+template <>
+struct Out<float> {
+  static __device__ __forceinline__ float get(const float* p) { return *p; }
+  static __device__ __forceinline__ void put(float* p, float v) { *p = v; }
+};
+template <>
+struct Out<__bf16> {
+  static __device__ __forceinline__ float get(const __bf16* p) { return (float)*p; }
+  static __device__ __forceinline__ void put(__bf16* p, float v) { *p = (__bf16)v; }
+};
+
+// Buffers are 16-byte aligned, so a run of more than 16 bytes is not known to be aligned further.
+template <typename T, int V>
+constexpr int kRunAlign = sizeof(T) * V < 16 ? sizeof(T) * V : 16;
+template <typename T, int V>
+__device__ __forceinline__ void put_run(T* p, const float (&v)[V]) {
+  T t[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) Out<T>::put(&t[i], v[i]);
+  __builtin_memcpy(__builtin_assume_aligned(p, (kRunAlign<T, V>)), t, sizeof(T) * V);
+}
+template <typename T, int V>
+__device__ __forceinline__ void get_run(const T* p, float (&v)[V]) {
+  T t[V];
+  __builtin_memcpy(t, __builtin_assume_aligned(p, (kRunAlign<T, V>)), sizeof(T) * V);
+#pragma unroll
+  for (int i = 0; i < V; ++i) v[i] = Out<T>::get(&t[i]);
+}
+
+// Stores V values (n0 + i < n) at p[0..], adding a residual first.
+template <typename T, int V>
+__device__ __forceinline__ void store_run(T* p, const T* res, float (&v)[V], int64_t left, bool vec) {
+  if (vec) {
+    if (res) {
+      float r[V];
+      get_run<T, V>(res, r);
+#pragma unroll
+      for (int i = 0; i < V; ++i) v[i] += r[i];
+    }
+    put_run<T, V>(p, v);
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+      if (i < left) Out<T>::put(p + i, res ? v[i] + Out<T>::get(res + i) : v[i]);
+  }
+}
+
+template <typename T, int V>
+__device__ __forceinline__ void epilogue_run(const MmEpilogue& ep, int64_t row, int group, int64_t n0,
+                                             float (&z)[V]) {
+  const int64_t left = ep.n - n0;
+  if (left <= 0) return;
+  const bool vec = ep.n % V == 0;
+  if (ep.bias) {
+    const int64_t at = (int64_t)group * ep.n + n0;
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+      if (i < left)
+        z[i] += ep.bias_f32 ? static_cast<const float*>(ep.bias)[at + i]
+                            : (float)static_cast<const __bf16*>(ep.bias)[at + i];
+  }
+  if (ep.z) store_run<T, V>(static_cast<T*>(ep.z) + row * ep.n + n0, nullptr, z, left, vec);
+  if (ep.act == kActSwiglu) {
+    float d[V / 2];
+#pragma unroll
+    for (int i = 0; i < V / 2; ++i) d[i] = z[2 * i] * sigmoid_f(z[2 * i]) * z[2 * i + 1];
+    const int64_t at = row * (ep.n / 2) + n0 / 2;
+    store_run<T, V / 2>(static_cast<T*>(ep.d) + at, ep.res ? static_cast<const T*>(ep.res) + at : nullptr, d,
+                        left / 2, vec);
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i) z[i] = act_f(z[i], ep.act);
+    const int64_t at = row * ep.n + n0;
+    store_run<T, V>(static_cast<T*>(ep.d) + at, ep.res ? static_cast<const T*>(ep.res) + at : nullptr, z, left,
+                    vec);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Token segments. Expert e owns rows [offsets[e], offsets[e + 1]), clamped to [0, rows].
+struct Segment {
+  int expert;
+  int64_t begin;  // first row of the expert
+  int64_t count;  // its rows
+  int tile;       // which of the expert's tiles
+};
+
+__device__ __forceinline__ int64_t clamp_row(int64_t v, int64_t rows) {
+  return v < 0 ? 0 : v > rows ? rows : v;
+}
+
+// Tiles of `step` rows over all segments, in expert order: their number.
+__device__ __forceinline__ int segment_tiles(const int64_t* offsets, int experts, int64_t rows, int step) {
+  const int lane = threadIdx.x & 63;
+  int sum = 0;
+  for (int e = lane; e < experts; e += 64) {
+    const int64_t c = clamp_row(offsets[e + 1], rows) - clamp_row(offsets[e], rows);
+    sum += c > 0 ? (int)((c + step - 1) / step) : 0;
+  }
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) sum += __shfl_xor(sum, d);
+  return __builtin_amdgcn_readfirstlane(sum);
+}
+
+// The segment that holds tile `index`; false past the last one. Every wave of a
+// workgroup finds it for itself: 64 experts a turn, an inclusive scan over the lanes.
+__device__ __forceinline__ bool find_segment(const int64_t* offsets, int experts, int64_t rows, int step, int index,
+                                             Segment& s) {
+  const int lane = threadIdx.x & 63;
+  int before = 0;
+  for (int e0 = 0; e0 < experts; e0 += 64) {
+    const int e = e0 + lane;
+    int64_t begin = 0, count = 0;
+    if (e < experts) {
+      begin = clamp_row(offsets[e], rows);
+      count = clamp_row(offsets[e + 1], rows) - begin;
+      if (count < 0) count = 0;
+    }
+    const int tiles = (int)((count + step - 1) / step);
+    int inc = tiles;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+      const int up = __shfl_up(inc, d);
+      if (lane >= d) inc += up;
+    }
+    const unsigned long long past = __ballot(inc > index - before);
+    if (past) {
+      const int at = __builtin_ctzll(past);
+      s.expert = e0 + at;
+      // rows < 2^31
+      s.begin = (uint32_t)__builtin_amdgcn_readlane((int)begin, at);
+      s.count = (uint32_t)__builtin_amdgcn_readlane((int)count, at);
+      s.tile = index - before - __builtin_amdgcn_readlane(inc - tiles, at);
+      return true;
+    }
+    before += __builtin_amdgcn_readlane(inc, 63);
+  }
+  return false;
+}
+
+}  // namespace mxq

@@ -1,0 +1,69 @@
+// Host-side launch interface of the matrix products and the epilogue's gradient.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+namespace mxq {
+
+enum Act : int { kActNone = 0, kActRelu = 1, kActGelu = 2, kActSilu = 3, kActSwiglu = 4 };
+
+struct MmEpilogue {
+  const void* bias;  // [groups, n] or null
+  const void* res;   // as d, or null
+  void* d;           // [rows, n], or [rows, n / 2] for kActSwiglu
+  void* z;           // [rows, n] or null
+  int64_t n;
+  int act;
+  int bias_f32, out_f32;
+};
+
+// One product. Dense: groups == 1 and offsets == null; grouped: `rows` tokens of
+// `groups` experts. fmt 0: MXFP4, 1: FP8.
+struct MmLaunch {
+  const uint8_t *a, *b;
+  const void *a_scales, *b_scales;
+  int a_fmt, b_fmt;
+  int64_t rows, n, k;
+  const int64_t* offsets;
+  int groups;
+  MmEpilogue ep;
+};
+
+hipError_t launch_gemm(const MmLaunch& a, hipStream_t st);
+
+struct WgradLaunch {
+  const uint8_t *y, *x;
+  const float *y_scales, *x_scales;
+  int64_t ld_y, ld_ys, ld_x, ld_xs;
+  int64_t rows, n, k;
+  const int64_t* offsets;
+  int experts;
+  const void* add;
+  void* d;
+  int out_f32;
+};
+
+hipError_t launch_grouped_wgrad(const WgradLaunch& a, hipStream_t st);
+
+struct ActGradLaunch {
+  const void *dy, *z;
+  int f32;
+  int64_t rows, n;
+  int act;
+  const int64_t* offsets;
+  int groups;
+  void* dz;
+  float* db;
+  float* partials;
+};
+
+// Rows that one workgroup of the activation gradient sums, and the row blocks that any
+// split of the rows into groups has at most.
+constexpr int kActGradRows = 64;
+constexpr int64_t act_grad_blocks(int64_t rows, int64_t groups) {
+  return (rows + (kActGradRows - 1) * groups) / kActGradRows;
+}
+hipError_t launch_act_grad(const ActGradLaunch& a, hipStream_t st);
+
+}  // namespace mxq

@@ -26,6 +26,9 @@ ROWWISE, COLWISE, BOTH = 1, 2, 3
 _FMT = {"mxfp4": MXFP4, "nvfp4": NVFP4, "nvfp4_2d": NVFP4_2D}
 _AXIS = {"row": ROWWISE, "col": COLWISE, "both": BOTH}
 _RND = {"rne": RNE, "sr": SR, "sr16": SR16}
+OPERAND_MXFP4, OPERAND_FP8 = 0, 1
+_ACT = {"none": 0, "relu": 1, "gelu": 2, "silu": 3, "swiglu": 4}
+SWIGLU = 4
 
 _lib = None
 
@@ -56,7 +59,13 @@ def lib() -> ctypes.CDLL:
     L.mxq_rht_signs.restype = u16
     L.mxq_status_string.argtypes = [i32]
     L.mxq_status_string.restype = ctypes.c_char_p
-    for name in ("mxq_quantize", "mxq_rht_quantize", "mxq_rht_quantize_mask", "mxq_dequantize", "mxq_fp8_to_mxfp4",
+    L.mxq_gemm.argtypes = [vp, vp, i32, vp, vp, i32, i64, i64, i64, vp, i32, i32, vp, vp, i32, vp, vp]
+    L.mxq_grouped_gemm.argtypes = [vp, vp, i32, vp, vp, i32, i64, i64, i64, vp, i64, vp, i32, i32, vp, vp, i32, vp, vp]
+    L.mxq_grouped_wgrad.argtypes = [vp, vp, i64, i64, vp, vp, i64, i64, i64, i64, i64, vp, i64, vp, vp, i32, vp]
+    L.mxq_act_grad.argtypes = [vp, vp, i32, i64, i64, i32, vp, i64, vp, vp, vp, vp]
+    L.mxq_act_grad_workspace.argtypes = [i64, i64, i64]
+    L.mxq_act_grad_workspace.restype = i64
+    for name in ("mxq_gemm", "mxq_grouped_gemm", "mxq_grouped_wgrad", "mxq_act_grad", "mxq_quantize", "mxq_rht_quantize", "mxq_rht_quantize_mask", "mxq_dequantize", "mxq_fp8_to_mxfp4",
                  "mxq_mxfp4_to_fp8", "mxq_fp4_row_to_fp8_col", "mxq_rht_apply", "mxq_amax", "mxq_rht_amax"):
         getattr(L, name).restype = i32
     _lib = L
@@ -247,3 +256,144 @@ def mxq_rht_amax(x: torch.Tensor, sign_mask: int, axis: str = "row",
     _check(lib().mxq_rht_amax(_ptr(x), _dtype_code(x), rows, cols, ldx, _AXIS[axis], sign_mask, _ptr(a),
                               _stream()))
     return a
+
+
+# ---------------------------------------------------------------------------
+# Matrix products (include/mxq_gemm.h). An operand is a pair (codes, scales): MXFP4 is
+# uint8 codes [R, K/2] with uint8 E8M0 bytes [R, K/32], FP8 is E4M3 bytes [R, K] with
+# fp32 scales [R, K/128]; for experts' weights [E, N, ...].
+
+def _operand(op, dims: int):
+    """(codes, scales, format, k) of an operand of `dims` dimensions, checked."""
+    codes, scales = op
+    if scales.dtype == torch.uint8:
+        fmt, k, want = OPERAND_MXFP4, codes.shape[-1] * 2, codes.shape[-1] // 16
+    elif scales.dtype == torch.float32:
+        fmt, k, want = OPERAND_FP8, codes.shape[-1], codes.shape[-1] // 128
+    else:
+        raise TypeError(f"unsupported scale dtype {scales.dtype}")
+    if codes.dtype != torch.uint8:
+        raise TypeError(f"unsupported code dtype {codes.dtype}")
+    if codes.dim() != dims or scales.dim() != dims or scales.shape[:-1] != codes.shape[:-1] or scales.shape[-1] != want:
+        raise ValueError(f"operand of {dims} dimensions expected, got codes {tuple(codes.shape)} and scales "
+                         f"{tuple(scales.shape)}")
+    if not (codes.is_contiguous() and scales.is_contiguous()):
+        raise ValueError("operands must be dense")
+    return codes, scales, fmt, k
+
+
+def _dense(t: Optional[torch.Tensor], shape, dtype, what: str) -> None:
+    if t is None:
+        return
+    if t.shape != shape or t.dtype != dtype or not t.is_contiguous():
+        raise ValueError(f"{what}: dense {dtype} {tuple(shape)} expected, got {t.dtype} {tuple(t.shape)}")
+
+
+def _offsets(offsets: torch.Tensor) -> int:
+    if offsets.dtype != torch.int64 or offsets.dim() != 1 or offsets.numel() < 2 or not offsets.is_contiguous():
+        raise ValueError("offsets: dense int64 [experts + 1] expected")
+    return offsets.numel() - 1
+
+
+def _product(a, b, offsets, bias, act, residual, preact, out_dtype, out):
+    ac, asc, afmt, k = _operand(a, 2)
+    bc, bsc, bfmt, bk = _operand(b, 2 if offsets is None else 3)
+    if bk != k:
+        raise ValueError(f"contracted dimensions differ: {k} and {bk}")
+    m, n, dev, code = ac.shape[0], bc.shape[-2], ac.device, _ACT[act]
+    dn = n // 2 if code == SWIGLU else n
+    d, z = out if out is not None else (None, None)
+    if d is None:
+        d = torch.empty((m, dn), dtype=out_dtype, device=dev)
+    else:
+        _dense(d, (m, dn), d.dtype, "out")
+    if preact and z is None:
+        z = torch.empty((m, n), dtype=d.dtype, device=dev)
+    _dense(z, (m, n), d.dtype, "z")
+    _dense(residual, (m, dn), d.dtype, "residual")
+    if bias is not None:
+        _dense(bias, bc.shape[:-1], bias.dtype, "bias")
+    dt, bdt = _dtype_code(d), F32 if bias is None else _dtype_code(bias)
+    if offsets is None:
+        _check(lib().mxq_gemm(_ptr(ac), _ptr(asc), afmt, _ptr(bc), _ptr(bsc), bfmt, m, n, k, _ptr(bias), bdt, code,
+                              _ptr(residual), _ptr(d), dt, _ptr(z), _stream()))
+    else:
+        experts = _offsets(offsets)
+        if bc.shape[0] != experts:
+            raise ValueError(f"{bc.shape[0]} weights for {experts} experts")
+        _check(lib().mxq_grouped_gemm(_ptr(ac), _ptr(asc), afmt, _ptr(bc), _ptr(bsc), bfmt, m, n, k, _ptr(offsets),
+                                      experts, _ptr(bias), bdt, code, _ptr(residual), _ptr(d), dt, _ptr(z), _stream()))
+    return (d, z) if preact else d
+
+
+def mxq_gemm(a, b, bias: Optional[torch.Tensor] = None, act: str = "none", residual: Optional[torch.Tensor] = None,
+             preact: bool = False, out_dtype=torch.bfloat16, out=None):
+    """mxq_gemm: d = act(A B^T + bias) + residual for operands a [M, K] and b [N, K] of
+    (codes, scales); act is "none", "relu", "gelu", "silu" or "swiglu" (rows of B in
+    gate/up pairs, d [M, N/2]). With `preact` the result is (d, z), z = A B^T + bias,
+    which mxq_act_grad takes. `out` = (d, z or None); residual may be d itself."""
+    return _product(a, b, None, bias, act, residual, preact, out_dtype, out)
+
+
+def mxq_grouped_gemm(a, b, offsets: torch.Tensor, bias: Optional[torch.Tensor] = None, act: str = "none",
+                     residual: Optional[torch.Tensor] = None, preact: bool = False, out_dtype=torch.bfloat16,
+                     out=None):
+    """mxq_grouped_gemm: mxq_gemm with the rows of a [R, K] grouped by expert (device
+    int64 offsets [E+1]), one weight b [E, N, K] and bias [E, N] per expert."""
+    return _product(a, b, offsets, bias, act, residual, preact, out_dtype, out)
+
+
+def mxq_grouped_wgrad(y, x, offsets: torch.Tensor, rows: int, add: Optional[torch.Tensor] = None,
+                      out_dtype=torch.bfloat16, out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """mxq_grouped_wgrad: per expert dW = dY^T X (+ add) over its tokens, from the FP8
+    columns that mxq_fp4_row_to_fp8_col returns: y = (q8 [N, >= rows], scales [N, S]),
+    x likewise [K, ...]; d [E, N, K]. `rows` tokens in all; add may be `out`."""
+    experts = _offsets(offsets)
+    slots = fp8_col_scale_slots(rows, experts)
+    for q8, s in (y, x):
+        if q8.dtype != torch.uint8 or s.dtype != torch.float32:
+            raise TypeError("FP8 columns are uint8 with fp32 scales")
+        if q8.dim() != 2 or s.dim() != 2 or s.shape[0] != q8.shape[0] or q8.shape[1] < rows or s.shape[1] < slots:
+            raise ValueError(f"columns of {rows} tokens and {slots} scales expected, got {tuple(q8.shape)} and "
+                             f"{tuple(s.shape)}")
+        if (q8.numel() and q8.stride(1) != 1) or (s.numel() and s.stride(1) != 1):
+            raise ValueError("columns must have unit token stride")
+    (yq, ys), (xq, xs) = y, x
+    n, k = yq.shape[0], xq.shape[0]
+    d = out if out is not None else torch.empty((experts, n, k), dtype=out_dtype, device=yq.device)
+    _dense(d, (experts, n, k), d.dtype, "out")
+    _dense(add, (experts, n, k), d.dtype, "add")
+    _check(lib().mxq_grouped_wgrad(_ptr(yq), _ptr(ys), yq.stride(0), ys.stride(0), _ptr(xq), _ptr(xs), xq.stride(0),
+                                   xs.stride(0), rows, n, k, _ptr(offsets), experts, _ptr(add), _ptr(d),
+                                   _dtype_code(d), _stream()))
+    return d
+
+
+def mxq_act_grad(dy: torch.Tensor, z: torch.Tensor, act: str = "none", offsets: Optional[torch.Tensor] = None,
+                 bias_grad: bool = False, out: Optional[torch.Tensor] = None, db: Optional[torch.Tensor] = None,
+                 workspace: Optional[torch.Tensor] = None):
+    """mxq_act_grad: dz = act'(z) dy for the z that a product kept, and with `bias_grad`
+    also the bias gradient: (dz, db), db fp32 [N], or [E, N] with expert offsets. `out`
+    may be z; `workspace` (uint8, mxq_act_grad_workspace bytes) is allocated if absent."""
+    rows, n = z.shape
+    code = _ACT[act]
+    _dense(z, (rows, n), z.dtype, "z")
+    _dense(dy, (rows, n // 2 if code == SWIGLU else n), z.dtype, "dy")
+    groups = 1 if offsets is None else _offsets(offsets)
+    dz = out if out is not None else torch.empty_like(z)
+    _dense(dz, z.shape, z.dtype, "out")
+    if bias_grad:
+        shape = (n,) if offsets is None else (groups, n)
+        if db is None:
+            db = torch.empty(shape, dtype=torch.float32, device=z.device)
+        _dense(db, shape, torch.float32, "db")
+        need = lib().mxq_act_grad_workspace(rows, n, groups)
+        if workspace is None:
+            workspace = torch.empty((need,), dtype=torch.uint8, device=z.device)
+        elif workspace.numel() * workspace.element_size() < need:
+            raise ValueError(f"workspace of {need} bytes expected")
+    else:
+        db = None
+    _check(lib().mxq_act_grad(_ptr(dy), _ptr(z), _dtype_code(z), rows, n, code, _ptr(offsets), groups, _ptr(dz),
+                              _ptr(db), _ptr(workspace), _stream()))
+    return (dz, db) if bias_grad else dz

@@ -1,0 +1,159 @@
+"""CPU-side checks of the matrix products' C ABI and binding: every declared entry point
+is exported, and invalid arguments are refused before the GPU is touched. No kernel is
+launched here."""
+import os
+import re
+
+import pytest
+import torch
+
+from mxfp4_microscaling_quantization_amd import mxq
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+FAKE = 0x10000  # a 16-byte aligned, never dereferenced address
+OK, EINVAL, ESHAPE, EALIGN, EUNSUPPORTED = (mxq.MXQ_OK, mxq.MXQ_EINVAL, mxq.MXQ_ESHAPE, mxq.MXQ_EALIGN,
+                                            mxq.MXQ_EUNSUPPORTED)
+
+
+def test_library_exports_every_declared_symbol():
+    text = open(os.path.join(ROOT, "include", "mxq_gemm.h")).read()
+    names = re.findall(r"^\s*(?:mxq_status|int64_t)\s+(mxq_\w+)\(", text, re.M)
+    assert sorted(names) == ["mxq_act_grad", "mxq_act_grad_workspace", "mxq_gemm", "mxq_grouped_gemm",
+                             "mxq_grouped_wgrad"]
+    for n in names:
+        assert hasattr(mxq.lib(), n), n
+
+
+def gemm(**kw):
+    a = dict(a=FAKE, asc=FAKE, af=0, b=FAKE, bsc=FAKE, bf=0, m=4, n=8, k=128, bias=None, bdt=1, act=0, res=None, d=FAKE,
+             ddt=0, z=None)
+    a.update(kw)
+    return mxq.lib().mxq_gemm(a["a"], a["asc"], a["af"], a["b"], a["bsc"], a["bf"], a["m"], a["n"], a["k"], a["bias"],
+                              a["bdt"], a["act"], a["res"], a["d"], a["ddt"], a["z"], None)
+
+
+def grouped(**kw):
+    a = dict(a=FAKE, asc=FAKE, af=0, b=FAKE, bsc=FAKE, bf=0, m=4, n=8, k=128, off=FAKE, E=2, bias=None, bdt=1, act=0,
+             res=None, d=FAKE, ddt=0, z=None)
+    a.update(kw)
+    return mxq.lib().mxq_grouped_gemm(a["a"], a["asc"], a["af"], a["b"], a["bsc"], a["bf"], a["m"], a["n"], a["k"],
+                                      a["off"], a["E"], a["bias"], a["bdt"], a["act"], a["res"], a["d"], a["ddt"],
+                                      a["z"], None)
+
+
+PRODUCT_REFUSALS = [
+    (dict(a=None), EINVAL), (dict(asc=None), EINVAL), (dict(b=None), EINVAL), (dict(bsc=None), EINVAL),
+    (dict(d=None), EINVAL), (dict(af=2), EINVAL), (dict(bf=-1), EINVAL), (dict(act=5), EINVAL), (dict(act=-1), EINVAL),
+    (dict(ddt=2), EINVAL), (dict(bias=FAKE, bdt=2), EINVAL), (dict(m=-1), EINVAL), (dict(n=-1), EINVAL),
+    (dict(k=-32), EINVAL), (dict(bf=1), EUNSUPPORTED),
+    (dict(n=0), ESHAPE), (dict(k=0), ESHAPE), (dict(k=48), ESHAPE), (dict(af=1, k=96), ESHAPE),
+    (dict(af=1, bf=1, k=160), ESHAPE), (dict(k=2 ** 22 + 32), ESHAPE), (dict(n=2 ** 31), ESHAPE),
+    (dict(m=2 ** 31), ESHAPE), (dict(act=4, n=9), ESHAPE), (dict(m=2 ** 30, n=2 ** 12), ESHAPE),
+    (dict(n=2 ** 30, k=2 ** 12), ESHAPE), (dict(m=2 ** 24, n=2 ** 16), ESHAPE),
+    (dict(a=FAKE + 8), EALIGN), (dict(b=FAKE + 4), EALIGN), (dict(d=FAKE + 2), EALIGN), (dict(res=FAKE + 8), EALIGN),
+    (dict(z=FAKE + 8), EALIGN), (dict(af=1, asc=FAKE + 2), EALIGN), (dict(af=1, bf=1, bsc=FAKE + 1), EALIGN),
+    (dict(bias=FAKE + 2), EALIGN), (dict(bias=FAKE + 1, bdt=0), EALIGN),
+    (dict(m=0, a=None, d=None), OK),
+]
+
+
+@pytest.mark.parametrize("kw,status", PRODUCT_REFUSALS)
+def test_product_refusals(kw, status):
+    assert gemm(**kw) == status
+    assert grouped(**kw) == status
+
+
+def test_grouped_refusals():
+    assert grouped(off=None) == EINVAL
+    assert grouped(E=0) == EINVAL
+    assert grouped(E=4097) == EINVAL
+    assert grouped(off=FAKE + 4) == EALIGN
+
+
+def wgrad(**kw):
+    a = dict(y=FAKE, ys=FAKE, ldy=304, ldys=10, x=FAKE, xs=FAKE, ldx=304, ldxs=10, rows=300, n=8, k=16, off=FAKE, E=4,
+             add=None, d=FAKE, ddt=0)
+    a.update(kw)
+    return mxq.lib().mxq_grouped_wgrad(a["y"], a["ys"], a["ldy"], a["ldys"], a["x"], a["xs"], a["ldx"], a["ldxs"],
+                                       a["rows"], a["n"], a["k"], a["off"], a["E"], a["add"], a["d"], a["ddt"], None)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(y=None), EINVAL), (dict(ys=None), EINVAL), (dict(x=None), EINVAL), (dict(xs=None), EINVAL),
+    (dict(d=None), EINVAL), (dict(off=None), EINVAL), (dict(ddt=3), EINVAL), (dict(rows=-1), EINVAL),
+    (dict(E=0), EINVAL), (dict(E=4097), EINVAL), (dict(n=0), ESHAPE), (dict(k=0), ESHAPE), (dict(ldy=288), ESHAPE),
+    (dict(ldx=0), ESHAPE), (dict(ldys=5), ESHAPE), (dict(ldxs=5), ESHAPE), (dict(n=2 ** 20, k=2 ** 21), ESHAPE),
+    (dict(n=2 ** 19, k=2 ** 21, E=4), ESHAPE), (dict(n=2 ** 31), ESHAPE), (dict(n=2 ** 18, k=2 ** 18, E=512), ESHAPE),
+    (dict(ldy=312), EALIGN), (dict(ldx=312), EALIGN), (dict(y=FAKE + 8), EALIGN), (dict(x=FAKE + 1), EALIGN),
+    (dict(ys=FAKE + 2), EALIGN), (dict(xs=FAKE + 2), EALIGN), (dict(off=FAKE + 4), EALIGN), (dict(add=FAKE + 4), EALIGN),
+    (dict(d=FAKE + 8), EALIGN),
+])
+def test_wgrad_refusals(kw, status):
+    # enough scale slots wherever the number of experts is not what is tested
+    if "E" in kw and kw["E"] > 4:
+        kw = dict(kw, ldys=4096, ldxs=4096)
+    assert wgrad(**kw) == status
+
+
+def act_grad(**kw):
+    a = dict(dy=FAKE, z=FAKE, dt=0, rows=4, n=8, act=1, off=None, E=1, dz=FAKE, db=None, ws=None)
+    a.update(kw)
+    return mxq.lib().mxq_act_grad(a["dy"], a["z"], a["dt"], a["rows"], a["n"], a["act"], a["off"], a["E"], a["dz"],
+                                  a["db"], a["ws"], None)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(dy=None), EINVAL), (dict(z=None), EINVAL), (dict(dz=None), EINVAL), (dict(db=FAKE), EINVAL),
+    (dict(dt=2), EINVAL), (dict(act=5), EINVAL), (dict(rows=-1), EINVAL), (dict(E=2), EINVAL),
+    (dict(off=FAKE, E=0), EINVAL), (dict(off=FAKE, E=4097), EINVAL), (dict(n=0), ESHAPE), (dict(act=4, n=7), ESHAPE),
+    (dict(n=2 ** 31), ESHAPE), (dict(rows=2 ** 21, n=2 ** 20), ESHAPE), (dict(dy=FAKE + 8), EALIGN),
+    (dict(z=FAKE + 4), EALIGN), (dict(dz=FAKE + 2), EALIGN), (dict(db=FAKE + 4, ws=FAKE), EALIGN),
+    (dict(db=FAKE, ws=FAKE + 8), EALIGN), (dict(off=FAKE + 4), EALIGN), (dict(rows=0, dy=None, z=None, dz=None), OK),
+])
+def test_act_grad_refusals(kw, status):
+    assert act_grad(**kw) == status
+
+
+def test_act_grad_workspace():
+    ws = mxq.lib().mxq_act_grad_workspace
+    assert ws(0, 8, 1) == 0 and ws(8, 0, 1) == 0 and ws(8, 8, 0) == 0 and ws(8, 8, 4097) == 0
+    # one row block per started 64 rows of every group: enough for any split
+    for rows, groups in ((1, 1), (64, 1), (65, 1), (300, 7), (5, 9)):
+        blocks = ws(rows, 10, groups) // 40
+        assert blocks >= (rows + 63) // 64
+        assert blocks >= min(rows, groups) - 1 + (rows - min(rows, groups) + 1 + 63) // 64
+
+
+U8, F32 = torch.uint8, torch.float32
+
+
+def cpu(shape, dtype=U8):
+    return torch.zeros(shape, dtype=dtype)
+
+
+@pytest.mark.parametrize("call,error", [
+    (lambda: mxq.mxq_gemm((cpu((4, 64)), cpu((4, 4))), (cpu((8, 32)), cpu((8, 2)))), ValueError),      # k differs
+    (lambda: mxq.mxq_gemm((cpu((4, 64)), cpu((4, 3))), (cpu((8, 64)), cpu((8, 4)))), ValueError),      # scales short
+    (lambda: mxq.mxq_gemm((cpu((4, 64)), cpu((3, 4))), (cpu((8, 64)), cpu((8, 4)))), ValueError),
+    (lambda: mxq.mxq_gemm((cpu((4, 128))[:, ::2], cpu((4, 4))), (cpu((8, 64)), cpu((8, 4)))), ValueError),
+    (lambda: mxq.mxq_gemm((cpu((4, 64)), cpu((4, 4), torch.int8)), (cpu((8, 64)), cpu((8, 4)))), TypeError),
+    (lambda: mxq.mxq_gemm((cpu((4, 64), torch.int8), cpu((4, 4))), (cpu((8, 64)), cpu((8, 4)))), TypeError),
+    (lambda: mxq.mxq_gemm((cpu((4, 64)), cpu((4, 4))), (cpu((8, 64)), cpu((8, 4))), bias=cpu((7,), F32)), ValueError),
+    (lambda: mxq.mxq_gemm((cpu((4, 64)), cpu((4, 4))), (cpu((8, 64)), cpu((8, 4))), residual=cpu((4, 8), F32)), ValueError),
+    (lambda: mxq.mxq_gemm((cpu((4, 64)), cpu((4, 4))), (cpu((8, 64)), cpu((8, 4))), out=(cpu((4, 7), F32), None)), ValueError),
+    (lambda: mxq.mxq_gemm((cpu((4, 64)), cpu((4, 4))), (cpu((8, 64)), cpu((8, 4))), out_dtype=torch.float16), TypeError),
+    (lambda: mxq.mxq_gemm((cpu((4, 64)), cpu((4, 4))), (cpu((8, 64)), cpu((8, 4))), act="tanh"), KeyError),
+    (lambda: mxq.mxq_grouped_gemm((cpu((4, 64)), cpu((4, 4))), (cpu((2, 8, 64)), cpu((2, 8, 4))),
+                                  torch.zeros(4, dtype=torch.int64)), ValueError),                      # 3 experts, 2 weights
+    (lambda: mxq.mxq_grouped_gemm((cpu((4, 64)), cpu((4, 4))), (cpu((2, 8, 64)), cpu((2, 8, 4))),
+                                  torch.zeros(3, dtype=torch.int32)), ValueError),
+    (lambda: mxq.mxq_grouped_wgrad((cpu((8, 16)), cpu((8, 1), F32)), (cpu((8, 16)), cpu((8, 2), F32)),
+                                   torch.zeros(3, dtype=torch.int64), 16), ValueError),                 # too few slots
+    (lambda: mxq.mxq_grouped_wgrad((cpu((8, 16)), cpu((8, 2), F32)), (cpu((8, 8)), cpu((8, 2), F32)),
+                                   torch.zeros(3, dtype=torch.int64), 16), ValueError),
+    (lambda: mxq.mxq_act_grad(cpu((4, 8), F32), cpu((4, 8), torch.bfloat16)), ValueError),
+    (lambda: mxq.mxq_act_grad(cpu((4, 8), F32), cpu((4, 8), F32), "swiglu"), ValueError),
+])
+def test_binding_refusals(call, error):
+    with pytest.raises(error):
+        call()
