@@ -147,6 +147,122 @@ __device__ __forceinline__ void epilogue_run(const MmEpilogue& ep, int64_t row, 
   }
 }
 
+// The same for one lane that finishes V fixed columns of many rows from sums in LDS:
+// bias, addresses and strides are set up once, and four rows are in flight together.
+template <typename T, int V>
+struct RunEpilogue {
+  float bias[V];
+  int64_t n0, dn, dcol;
+  int left;
+  bool vec, gated;
+
+  __device__ __forceinline__ RunEpilogue(const MmEpilogue& ep, int group, int64_t first) : n0(first) {
+    gated = ep.act == kActSwiglu;
+    dn = gated ? ep.n / 2 : ep.n;
+    dcol = gated ? first / 2 : first;
+    left = ep.n - first < V ? (int)(ep.n - first) : V;
+    vec = ep.n % V == 0;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      bias[i] = 0.0f;
+      if (ep.bias && i < left) {
+        const int64_t at = (int64_t)group * ep.n + first + i;
+        bias[i] = ep.bias_f32 ? static_cast<const float*>(ep.bias)[at] : (float)static_cast<const __bf16*>(ep.bias)[at];
+      }
+    }
+  }
+
+  // Rows row, row + step, ... (count of them, those from `rows` on missing), their sums at
+  // z, z + zstep, ...
+  __device__ __forceinline__ void rows(const MmEpilogue& ep, const float* z, int zstep, int64_t row, int rows, int step,
+                                       int count) {
+    constexpr int U = 4;
+    if (left <= 0) return;
+    T* d = static_cast<T*>(ep.d) + row * dn + dcol;
+    const T* res = static_cast<const T*>(ep.res) + row * dn + dcol;
+    T* keep = static_cast<T*>(ep.z) + row * ep.n + n0;
+    const int64_t dstep = step * dn, kstep = step * ep.n;
+#pragma unroll 1
+    for (int u = 0; u < count; u += U) {
+      float v[U][V], r[U][V];
+#pragma unroll
+      for (int k = 0; k < U; ++k)
+#pragma unroll
+        for (int i = 0; i < V; ++i) v[k][i] = z[k * zstep + i];
+      if (ep.res && vec) {
+#pragma unroll
+        for (int k = 0; k < U; ++k) {
+          if ((u + k) * step < rows) {
+            if (gated) {
+              float half[V / 2];
+              get_run<T, V / 2>(res + k * dstep, half);
+#pragma unroll
+              for (int i = 0; i < V / 2; ++i) r[k][i] = half[i];
+            } else {
+              get_run<T, V>(res + k * dstep, r[k]);
+            }
+          }
+        }
+      }
+      if (ep.bias) {
+#pragma unroll
+        for (int k = 0; k < U; ++k)
+#pragma unroll
+          for (int i = 0; i < V; ++i) v[k][i] += bias[i];
+      }
+      if (ep.z) {
+#pragma unroll
+        for (int k = 0; k < U; ++k)
+          if ((u + k) * step < rows) store_run<T, V>(keep + k * kstep, nullptr, v[k], left, vec);
+      }
+      if (gated) {
+#pragma unroll
+        for (int k = 0; k < U; ++k) {
+          float g[V / 2];
+#pragma unroll
+          for (int i = 0; i < V / 2; ++i) {
+            g[i] = v[k][2 * i] * sigmoid_f(v[k][2 * i]) * v[k][2 * i + 1];
+            if (ep.res && vec) g[i] += r[k][i];
+          }
+          if ((u + k) * step < rows)
+            store_run<T, V / 2>(d + k * dstep, vec || !ep.res ? nullptr : res + k * dstep, g, left / 2, vec);
+        }
+      } else {
+        act_runs<U>(v, ep.act);
+#pragma unroll
+        for (int k = 0; k < U; ++k) {
+          if (ep.res && vec) {
+#pragma unroll
+            for (int i = 0; i < V; ++i) v[k][i] += r[k][i];
+          }
+          if ((u + k) * step < rows)
+            store_run<T, V>(d + k * dstep, vec || !ep.res ? nullptr : res + k * dstep, v[k], left, vec);
+        }
+      }
+      z += U * zstep;
+      d += U * dstep;
+      res += U * dstep;
+      keep += U * kstep;
+    }
+  }
+
+  template <int U>
+  static __device__ __forceinline__ void act_runs(float (&v)[U][V], int act) {
+    if (act == kActNone) return;
+#pragma unroll
+    for (int k = 0; k < U; ++k)
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        if (act == kActRelu)
+          v[k][i] = v[k][i] < 0.0f ? 0.0f : v[k][i];
+        else if (act == kActGelu)
+          v[k][i] = gelu_f(v[k][i]);
+        else
+          v[k][i] = v[k][i] * sigmoid_f(v[k][i]);
+      }
+  }
+};
+
 // ---------------------------------------------------------------------------
 // Token segments. Expert e owns rows [offsets[e], offsets[e + 1]), clamped to [0, rows].
 struct Segment {

@@ -153,6 +153,7 @@ __global__ __launch_bounds__(64) void wgrad_wave_kernel(WgradLaunch p, int col_t
 }  // namespace
 
 hipError_t launch_gemm(const MmLaunch& a, hipStream_t st) {
+  if (a.rows > 32) return launch_gemm_tiles(a, a.rows >= 200, st);
   if (a.a_fmt && a.b_fmt) return launch_wave<true, true>(a, st);
   if (a.a_fmt) return launch_wave<true, false>(a, st);
   return launch_wave<false, false>(a, st);

@@ -30,6 +30,8 @@ struct MmLaunch {
   MmEpilogue ep;
 };
 
+// The tiled kernel: 256 x 256 results of a workgroup (large) or 128 x 128.
+hipError_t launch_gemm_tiles(const MmLaunch& a, bool large, hipStream_t st);
 hipError_t launch_gemm(const MmLaunch& a, hipStream_t st);
 
 struct WgradLaunch {
