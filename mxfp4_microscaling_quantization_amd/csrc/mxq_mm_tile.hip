@@ -6,25 +6,30 @@ namespace mxq {
 
 namespace {
 
-// A workgroup of four waves (2 x 2) owns 64 MI x 64 NI results, a wave 32 MI x 32 NI.
-// The contraction runs in stages of 128 elements: 64 bytes of an MXFP4 row, 128 of an
-// FP8 row. A ring of stages in LDS is filled by loads that write LDS directly; a
-// stage's slot is refilled once every wave has read its last fragments into registers.
-// Fragments of the next half stage are read from LDS while the matrix cores work on
-// the current one, so one barrier a stage is all that the waves wait for.
-template <bool A8, bool B8, int MI, int NI>
+// A workgroup of 2 x WN waves owns 64 MI x 32 NI WN results, a wave 32 MI x 32 NI. The
+// contraction runs in steps of 64 elements, two to a unit of 128. Each operand has a ring
+// of four slots in LDS, 64 bytes of a row in each: a unit of an MXFP4 row or a step of
+// an FP8 row. Direct loads fill the slots three ahead, evenly over the steps: a burst
+// would stall the waves at the memory pipe's door. Fragments of the next step are read
+// from LDS while the matrix cores work on the current one; one barrier a slot (every unit,
+// with FP8 every step) is all that the waves wait for.
+template <bool A8, bool B8, int MI, int NI, int WN>
 struct Tile {
-  static constexpr int BM = 64 * MI, BN = 64 * NI;
-  static constexpr int RA = A8 ? 128 : 64, RB = B8 ? 128 : 64;  // bytes of a row in a stage
-  static constexpr int ABytes = BM * RA, Stage = BM * RA + BN * RB;
-  static constexpr int Ring = A8 && B8 ? 2 : A8 ? 3 : 4;
-  static constexpr int DA = BM * RA / 4096, DB = BN * RB / 4096;  // 1 KiB loads of a wave in a stage
-  // scales: 16 bytes of a row cover four stages; two such chunks
+  static constexpr int Waves = 2 * WN, Threads = 64 * Waves;
+  static constexpr int BM = 64 * MI, BN = 32 * NI * WN;
+  static constexpr int Ring = 4, ASlot = BM * 64, BSlot = BN * 64;
+  static constexpr int BRing = Ring * ASlot, SRing = BRing + Ring * BSlot;  // offsets in LDS
+  static constexpr int DA = ASlot / 1024 / Waves, DB = BSlot / 1024 / Waves;  // 1 KiB loads of a wave for a slot
+  // loads of a step, and those younger than the slot a barrier waits for
+  static constexpr int Issued = (A8 ? DA : DA / 2) + (B8 ? DB : DB / 2);
+  static constexpr int Younger = A8 ? Issued : 3 * Issued;
+  // scales: 16 bytes of a row cover a chunk of four units; two such chunks
   static constexpr int SRows = BM + BN, SChunk = SRows * 16;
-  static constexpr int SLoads = SRows / 64;  // 256-byte loads of a wave in a chunk (16 rows each)
-  static constexpr int Lds = Ring * Stage + 2 * SChunk;
+  static constexpr int SLoads = SRows / 16 / Waves;  // 256-byte loads of a wave in a chunk (16 rows each)
+  static constexpr int Lds = SRing + 2 * SChunk;
   static constexpr int PadN = 32 * NI + 4;  // floats of a row parked for the epilogue
-  static_assert(4 * (MI > 2 ? 2 : MI) * 32 * PadN * 4 <= Lds, "the epilogue's rows fit");
+  static_assert(DA % 2 == 0 && DB % 2 == 0, "half a slot is whole loads");
+  static_assert(Waves * (MI > 2 ? 2 : MI) * 32 * PadN * 4 <= Lds, "the epilogue's rows fit");
 };
 
 __device__ __forceinline__ v4i buffer_of(const void* base, int64_t bytes) {
@@ -56,28 +61,24 @@ __device__ __forceinline__ void barrier() {
   asm volatile("s_barrier" ::: "memory");
 }
 
-// Which 16-byte piece of a row's stage holds logical piece c: rows are spread over the
-// banks so that the 32 rows of a fragment read collide in none.
-template <int R>
-__device__ __forceinline__ int piece(int row, int c) {
-  return R == 64 ? c ^ ((row >> 2) & 3) : c ^ ((row >> 1) & 7);
-}
+// Which 16-byte piece of a row's slot holds logical piece c: rows are spread over the
+// banks so that the reads of a fragment collide in none.
+__device__ __forceinline__ int piece(int row, int c) { return c ^ ((row >> 2) & 3); }
 
 template <bool FP8>
 struct Frag {
   v4i w[FP8 ? 2 : 1];
 };
 
-// Fragment of rows [row0, row0 + 32) for half stage s.
+// This lane's row of a fragment for step s of a unit, from the slot that holds it.
 template <bool FP8, bool EXACT>
-__device__ __forceinline__ Frag<FP8> read_frag(const uint8_t* lds, int row, int s, int h) {
-  constexpr int R = FP8 ? 128 : 64;
+__device__ __forceinline__ Frag<FP8> read_frag(const uint8_t* slot, int row, int s, int h) {
   Frag<FP8> f;
   if constexpr (FP8) {
-    f.w[0] = *reinterpret_cast<const v4i*>(lds + row * R + 16 * piece<R>(row, 4 * s + (EXACT ? 2 * h : h)));
-    f.w[1] = *reinterpret_cast<const v4i*>(lds + row * R + 16 * piece<R>(row, 4 * s + (EXACT ? 2 * h + 1 : 2 + h)));
+    f.w[0] = *reinterpret_cast<const v4i*>(slot + row * 64 + 16 * piece(row, EXACT ? 2 * h : h));
+    f.w[1] = *reinterpret_cast<const v4i*>(slot + row * 64 + 16 * piece(row, EXACT ? 2 * h + 1 : 2 + h));
   } else {
-    f.w[0] = *reinterpret_cast<const v4i*>(lds + row * R + 16 * piece<R>(row, 2 * s + h));
+    f.w[0] = *reinterpret_cast<const v4i*>(slot + row * 64 + 16 * piece(row, 2 * s + h));
   }
   return f;
 }
@@ -98,14 +99,14 @@ __device__ __forceinline__ bf16x8 bf16_of(const Frag<FP8>& f, int j, float scale
     return bf16_from_e2m1((uint32_t)f.w[0][j], scale);
 }
 
-// The scale register of a stage: MXFP4 byte 0 (2) is the block of this lane half in half
-// stage 0 (1); FP8 byte 0 is the group's exponent.
+// The scale register of a unit: MXFP4 byte 0 (2) is the block of this lane half in the
+// first (second) step; FP8 byte 0 is the group's exponent.
 template <bool FP8>
 __device__ __forceinline__ uint32_t scale_reg(uint32_t raw, int h) {
   return FP8 ? raw >> 23 : raw >> (8 * h);
 }
 
-// One half stage on the matrix cores. `between` is called MI times in the course of it
+// One step on the matrix cores, the first (S = 0) or second of a unit. `between` is called MI times in the course of it
 // (with 0 .. MI - 1) to issue loads while the matrix cores are busy.
 template <bool A8, bool B8, bool EXACT, int MI, int NI, int S, typename F>
 __device__ __forceinline__ void multiply(f32x16 (&c)[MI][NI], const Frag<A8> (&a)[MI], const Frag<B8> (&b)[NI],
@@ -152,9 +153,9 @@ __device__ __forceinline__ int xcd_order(int b, int total) {
   return x * q + (x < r ? x : r) + (b >> 3);
 }
 
-template <bool A8, bool B8, bool EXACT, int MI, int NI, bool ODDK, typename T>
-__global__ __launch_bounds__(256, MI *NI > 4 ? 1 : 2) void mm_tile_kernel(MmLaunch p, int col_tiles) {
-  using G = Tile<A8, B8, MI, NI>;
+template <bool A8, bool B8, bool EXACT, int MI, int NI, int WN, bool ODDK, typename T>
+__global__ __launch_bounds__(128 * WN, MI *NI > 8 ? 1 : 2) void mm_tile_kernel(MmLaunch p, int col_tiles) {
+  using G = Tile<A8, B8, MI, NI, WN>;
   extern __shared__ __align__(16) uint8_t lds[];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r = lane & 31, h = lane >> 5;
@@ -185,74 +186,86 @@ __global__ __launch_bounds__(256, MI *NI > 4 ? 1 : 2) void mm_tile_kernel(MmLaun
   const v4i asbuf = buffer_of(ascale, arows * asbytes);
   const v4i bsbuf = buffer_of(bscale, brows * bsbytes);
 
-  // byte offsets of this lane's pieces in the stages' loads; rows past the end repeat the last
+  // byte offsets of this lane's pieces in the slots' loads; rows past the end repeat the last
   uint32_t va[G::DA], vb[G::DB];
 #pragma unroll
   for (int j = 0; j < G::DA; ++j) {
-    const int row = ((wave * G::DA + j) * 64 + lane) * 16 / G::RA, c = lane % (G::RA / 16);
-    va[j] = (uint32_t)((row < arows ? row : arows - 1) * abytes) + 16 * piece<G::RA>(row, c);
+    const int row = (wave * G::DA + j) * 16 + lane / 4;
+    va[j] = (uint32_t)((row < arows ? row : arows - 1) * abytes) + 16 * piece(row, lane % 4);
   }
 #pragma unroll
   for (int j = 0; j < G::DB; ++j) {
-    const int row = ((wave * G::DB + j) * 64 + lane) * 16 / G::RB, c = lane % (G::RB / 16);
-    vb[j] = (uint32_t)((row < brows ? row : brows - 1) * bbytes) + 16 * piece<G::RB>(row, c);
+    const int row = (wave * G::DB + j) * 16 + lane / 4;
+    vb[j] = (uint32_t)((row < brows ? row : brows - 1) * bbytes) + 16 * piece(row, lane % 4);
   }
   const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)lds;
-  const int stages = (int)((p.k + 127) / 128);
-  const int tail = ODDK ? (int)(p.k % 128) / 32 : 0;  // blocks of the last stage, 0: all four
+  const int units = (int)((p.k + 127) / 128);
+  const int tail = (int)(p.k % 128) / 32;  // blocks of the last unit, 0: all four (MXFP4 only: ODDK)
 
-  // Part u of MI of the loads of stage t (past the last stage: loads of nothing, so that
-  // every stage has the same number outstanding).
-  auto load_stage = [&](int t, int u) {
-    const uint32_t slot = lds0 + (uint32_t)(t % G::Ring) * G::Stage;
-    v4i ab = abuf, bb = bbuf;
-    ab[2] = t < stages ? ab[2] : 0;
-    bb[2] = t < stages ? bb[2] : 0;
-    const bool cut = ODDK && tail && t == stages - 1;
+  // Before the last unit is loaded: pieces past the rows' end repeat the row's first one.
+  auto trim = [&](int t) {
+    if (ODDK && tail && t == units - 1) {
 #pragma unroll
-    for (int j = u * G::DA / MI; j < (u + 1) * G::DA / MI; ++j) {
-      uint32_t v = va[j];
-      if (cut) {  // pieces past the row's end repeat its first one of the stage
-        const int row = ((wave * G::DA + j) * 64 + lane) * 16 / G::RA, c = piece<G::RA>(row, lane % (G::RA / 16));
-        v -= c >= tail ? 16 * c : 0;
+      for (int j = 0; j < G::DA; ++j) {
+        const int c = piece((wave * G::DA + j) * 16 + lane / 4, lane % 4);
+        va[j] -= c >= tail ? 16 * c : 0;
       }
-      load_lds16(ab, v, (uint32_t)t * G::RA, slot + (wave * G::DA + j) * 1024);
-    }
 #pragma unroll
-    for (int j = u * G::DB / MI; j < (u + 1) * G::DB / MI; ++j) {
-      uint32_t v = vb[j];
-      if (cut) {
-        const int row = ((wave * G::DB + j) * 64 + lane) * 16 / G::RB, c = piece<G::RB>(row, lane % (G::RB / 16));
-        v -= c >= tail ? 16 * c : 0;
+      for (int j = 0; j < G::DB; ++j) {
+        const int c = piece((wave * G::DB + j) * 16 + lane / 4, lane % 4);
+        vb[j] -= c >= tail ? 16 * c : 0;
       }
-      load_lds16(bb, v, (uint32_t)t * G::RB, slot + G::ABytes + (wave * G::DB + j) * 1024);
     }
   };
+  // Loads j0 <= j < j1 of slot number q of A (of B): unit q of an MXFP4 operand, step q of an
+  // FP8 one. Past the last slot they load nothing, so that every step has the same number
+  // outstanding.
+  auto load_a = [&](int q, int j0, int j1) {
+    v4i buf = abuf;
+    buf[2] = q < (A8 ? 2 * units : units) ? buf[2] : 0;
+#pragma unroll
+    for (int j = j0; j < j1; ++j)
+      load_lds16(buf, va[j], (uint32_t)q * 64, lds0 + (q & 3) * G::ASlot + (wave * G::DA + j) * 1024);
+  };
+  auto load_b = [&](int q, int j0, int j1) {
+    v4i buf = bbuf;
+    buf[2] = q < (B8 ? 2 * units : units) ? buf[2] : 0;
+#pragma unroll
+    for (int j = j0; j < j1; ++j)
+      load_lds16(buf, vb[j], (uint32_t)q * 64, lds0 + G::BRing + (q & 3) * G::BSlot + (wave * G::DB + j) * 1024);
+  };
+  // Part u of MI of the loads issued in step s of unit t.
+  auto load_part = [&](int t, int s, int u) {
+    constexpr int NA = A8 ? G::DA : G::DA / 2, NB = B8 ? G::DB : G::DB / 2;
+    const int a0 = A8 ? 0 : s * NA, b0 = B8 ? 0 : s * NB;
+    load_a(A8 ? 2 * t + s + 3 : t + 3, a0 + u * NA / MI, a0 + (u + 1) * NA / MI);
+    load_b(B8 ? 2 * t + s + 3 : t + 3, b0 + (u * NB + MI - 1) / MI, b0 + ((u + 1) * NB + MI - 1) / MI);
+  };
 
-  uint8_t* const sring = lds + G::Ring * G::Stage;
-  // Chunk c of the scales: the dwords of stages 4c..4c + 3 of every row, by direct loads.
-  // A stage past the last one repeats the last one's dword.
+  uint8_t* const sring = lds + G::SRing;
+  // Chunk c of the scales: four dwords of every row, by direct loads. A dword past the
+  // row's end repeats its last one.
   auto load_scales = [&](int c) {
-    const uint32_t slot = lds0 + G::Ring * G::Stage + (uint32_t)(c & 1) * G::SChunk;
-    const int want = 4 * c + (lane & 3), stage = want < stages ? want : stages - 1;
+    const uint32_t slot = lds0 + G::SRing + (uint32_t)(c & 1) * G::SChunk;
+    const int want = 4 * c + (lane & 3), most = (int)(p.k / 128) - 1, dword = want < most ? want : most;
 #pragma unroll
     for (int j = 0; j < G::SLoads; ++j) {
       const int first = (wave * G::SLoads + j) * 16;  // uniform: 16 rows of A or of B
       const int row = first + (lane >> 2);
       if (first < G::BM)
-        load_lds4(asbuf, (uint32_t)((row < arows ? row : arows - 1) * asbytes) + 4 * stage, 0, slot + first * 16);
+        load_lds4(asbuf, (uint32_t)((row < arows ? row : arows - 1) * asbytes) + 4 * dword, 0, slot + first * 16);
       else
-        load_lds4(bsbuf, (uint32_t)((row - G::BM < brows ? row - G::BM : brows - 1) * bsbytes) + 4 * stage, 0,
+        load_lds4(bsbuf, (uint32_t)((row - G::BM < brows ? row - G::BM : brows - 1) * bsbytes) + 4 * dword, 0,
                   slot + first * 16);
     }
   };
   // The same through registers where rows of block bytes do not start on dwords.
-  constexpr int SR = G::SRows / 256 > 0 ? G::SRows / 256 : 1;
+  constexpr int SR = (G::SRows + G::Threads - 1) / G::Threads;
   v4i held[SR];
   auto fetch_scales = [&](int c) {
 #pragma unroll
     for (int j = 0; j < SR; ++j) {
-      const int row = threadIdx.x + 256 * j;
+      const int row = threadIdx.x + G::Threads * j;
       if (row < G::SRows) {
         const bool is_a = row < G::BM;
         const int rr = is_a ? (row < arows ? row : arows - 1) : (row - G::BM < brows ? row - G::BM : brows - 1);
@@ -278,36 +291,38 @@ __global__ __launch_bounds__(256, MI *NI > 4 ? 1 : 2) void mm_tile_kernel(MmLaun
   auto park_scales = [&](int c) {
 #pragma unroll
     for (int j = 0; j < SR; ++j) {
-      const int row = threadIdx.x + 256 * j;
+      const int row = threadIdx.x + G::Threads * j;
       if (row < G::SRows) *reinterpret_cast<v4i*>(sring + (c & 1) * G::SChunk + row * 16) = held[j];
     }
   };
-  // Clears the pieces of the last stage that lie past the rows' end.
+  // The last unit's last step has one block where `tail` is odd: clears the other one.
   auto clear_tail = [&]() {
-    uint8_t* slot = lds + ((stages - 1) % G::Ring) * G::Stage;
-    for (int i = threadIdx.x; i < G::SRows * 4; i += 256) {
-      const int row = i >> 2, c = i & 3;
-      if (c >= tail) *reinterpret_cast<v4i*>(slot + row * 64 + 16 * piece<64>(row, c)) = v4i{0, 0, 0, 0};
+    uint8_t* a = lds + ((units - 1) & 3) * G::ASlot;
+    uint8_t* b = lds + G::BRing + ((units - 1) & 3) * G::BSlot;
+    for (int row = threadIdx.x; row < G::SRows; row += G::Threads) {
+      const int x = row < G::BM ? row : row - G::BM;
+      *reinterpret_cast<v4i*>((row < G::BM ? a : b) + x * 64 + 16 * piece(x, tail)) = v4i{0, 0, 0, 0};
     }
     wait_loads<0>();
     barrier();
   };
 
-  const int wm = wave >> 1, wn = wave & 1;
+  const int wm = wave / WN, wn = wave % WN;
   const int arow = wm * 32 * MI + r, brow = wn * 32 * NI + r;
   Frag<A8> fa[2][MI];
   Frag<B8> fb[2][NI];
   uint32_t sa[MI], sb[NI], ra[MI], rb[NI];
   f32x16 c[MI][NI] = {};
 
-  auto read_half = [&](int t, int half, Frag<A8>(&xa)[MI], Frag<B8>(&xb)[NI]) {
-    const uint8_t* slot = lds + (t % G::Ring) * G::Stage;
+  auto read_step = [&](int t, int s, Frag<A8>(&xa)[MI], Frag<B8>(&xb)[NI]) {
+    const uint8_t* a = lds + ((A8 ? 2 * t + s : t) & 3) * G::ASlot;
+    const uint8_t* b = lds + G::BRing + ((B8 ? 2 * t + s : t) & 3) * G::BSlot;
 #pragma unroll
-    for (int i = 0; i < MI; ++i) xa[i] = read_frag<A8, EXACT>(slot, arow + 32 * i, half, h);
+    for (int i = 0; i < MI; ++i) xa[i] = read_frag<A8, EXACT>(a, arow + 32 * i, s, h);
 #pragma unroll
-    for (int j = 0; j < NI; ++j) xb[j] = read_frag<B8, EXACT>(slot + G::ABytes, brow + 32 * j, half, h);
+    for (int j = 0; j < NI; ++j) xb[j] = read_frag<B8, EXACT>(b, brow + 32 * j, s, h);
   };
-  // The scales of stage t as they lie in LDS; select() makes them the instructions' operands.
+  // The scales of unit t as they lie in LDS; select_scales makes them the instructions'.
   auto read_scales = [&](int t) {
     const uint8_t* q = sring + ((t >> 2) & 1) * G::SChunk + 4 * (t & 3);
 #pragma unroll
@@ -329,43 +344,57 @@ __global__ __launch_bounds__(256, MI *NI > 4 ? 1 : 2) void mm_tile_kernel(MmLaun
   } else {
     load_scales(0);
   }
-  for (int t = 0; t < G::Ring; ++t)
 #pragma unroll
-    for (int u = 0; u < MI; ++u) load_stage(t, u);
-  wait_loads<(G::Ring - 1) * (G::DA + G::DB)>();
+  for (int q = 0; q < 3; ++q) {
+    trim(q);
+    load_a(q, 0, G::DA);
+    load_b(q, 0, G::DB);
+  }
+  wait_loads<2 * (G::DA + G::DB)>();
   barrier();
-  if (ODDK && tail && stages == 1) clear_tail();
-  read_half(0, 0, fa[0], fb[0]);
+  if (ODDK && (tail & 1) && units == 1) clear_tail();
+  read_step(0, 0, fa[0], fb[0]);
   read_scales(0);
   select_scales();
 
-  for (int t = 0; t + 1 < stages; ++t) {
-    read_half(t, 1, fa[1], fb[1]);
-    if constexpr (ODDK) {
-      // chunk c + 1 is fetched in the first stage of chunk c and parked in the third
-      if ((t & 3) == 0 && t + 4 < stages) fetch_scales((t >> 2) + 1);
-      if ((t & 3) == 2 && t + 2 < stages) park_scales((t >> 2) + 1);
+  for (int t = 0; t + 1 < units; ++t) {
+    // first step
+    if constexpr (A8) {
+      wait_loads<G::Younger>();
+      barrier();
     }
+    trim(t + 3);
+    if constexpr (ODDK) {
+      // chunk c + 1 is fetched in the first unit of chunk c and parked in the third
+      if ((t & 3) == 0 && t + 4 < units) fetch_scales((t >> 2) + 1);
+      if ((t & 3) == 2 && t + 2 < units) park_scales((t >> 2) + 1);
+    } else {
+      if ((t & 3) == 0 && t + 4 < units) load_scales((t >> 2) + 1);
+    }
+    read_step(t, 1, fa[1], fb[1]);
     __builtin_amdgcn_sched_barrier(0);
-    multiply<A8, B8, EXACT, MI, NI, 0>(c, fa[0], fb[0], sa, sb, idle);
+    multiply<A8, B8, EXACT, MI, NI, 0>(c, fa[0], fb[0], sa, sb, [&](int u) { load_part(t, 0, u); });
     __builtin_amdgcn_sched_barrier(0);
-    // stage t + 1 has landed once at most the later stages' loads are outstanding; every
-    // wave has the last fragments of stage t
-    wait_loads<(G::Ring - 2) * (G::DA + G::DB)>();
+    // second step: the next slots have landed once at most the younger loads are outstanding,
+    // and every wave has read its last fragments of the slots that are filled next
+    wait_loads<G::Younger>();
     barrier();
-    if (ODDK && tail && t + 2 == stages) clear_tail();
-    if constexpr (!ODDK)
-      if ((t & 3) == 0 && t + 4 < stages) load_scales((t >> 2) + 1);
-    read_half(t + 1, 0, fa[0], fb[0]);
+    if (ODDK && (tail & 1) && t + 2 == units) clear_tail();
+    read_step(t + 1, 0, fa[0], fb[0]);
     read_scales(t + 1);
     __builtin_amdgcn_sched_barrier(0);
-    multiply<A8, B8, EXACT, MI, NI, 1>(c, fa[1], fb[1], sa, sb, [&](int u) { load_stage(t + G::Ring, u); });
+    multiply<A8, B8, EXACT, MI, NI, 1>(c, fa[1], fb[1], sa, sb, [&](int u) { load_part(t, 1, u); });
     __builtin_amdgcn_sched_barrier(0);
     select_scales();
   }
-  read_half(stages - 1, 1, fa[1], fb[1]);
+  if constexpr (A8) {
+    wait_loads<G::Younger>();
+    barrier();
+  }
+  const bool both = !ODDK || tail == 0 || tail > 2;
+  if (both) read_step(units - 1, 1, fa[1], fb[1]);
   multiply<A8, B8, EXACT, MI, NI, 0>(c, fa[0], fb[0], sa, sb, idle);
-  multiply<A8, B8, EXACT, MI, NI, 1>(c, fa[1], fb[1], sa, sb, idle);
+  if (both) multiply<A8, B8, EXACT, MI, NI, 1>(c, fa[1], fb[1], sa, sb, idle);
 
   // Epilogue: a block of rows at a time through LDS, so that rows leave as whole runs.
   wait_loads<0>();
@@ -397,40 +426,40 @@ __global__ __launch_bounds__(256, MI *NI > 4 ? 1 : 2) void mm_tile_kernel(MmLaun
   }
 }
 
-template <bool A8, bool B8, bool EXACT, int MI, int NI, bool ODDK, typename T>
+template <bool A8, bool B8, bool EXACT, int MI, int NI, int WN, bool ODDK, typename T>
 hipError_t launch_tile(const MmLaunch& a, hipStream_t st) {
-  using G = Tile<A8, B8, MI, NI>;
+  using G = Tile<A8, B8, MI, NI, WN>;
   const int64_t col_tiles = (a.n + G::BN - 1) / G::BN;
   const int64_t row_tiles = a.offsets ? a.rows / G::BM + (a.rows < a.groups ? a.rows : a.groups)
                                       : (a.rows + G::BM - 1) / G::BM;
-  auto k = mm_tile_kernel<A8, B8, EXACT, MI, NI, ODDK, T>;
+  auto k = mm_tile_kernel<A8, B8, EXACT, MI, NI, WN, ODDK, T>;
   static const hipError_t set =
       hipFuncSetAttribute(reinterpret_cast<const void*>(k), hipFuncAttributeMaxDynamicSharedMemorySize, G::Lds);
   if (set != hipSuccess) return set;
-  k<<<dim3((uint32_t)(row_tiles * col_tiles)), 256, G::Lds, st>>>(a, (int)col_tiles);
+  k<<<dim3((uint32_t)(row_tiles * col_tiles)), G::Threads, G::Lds, st>>>(a, (int)col_tiles);
   return hipGetLastError();
 }
 
-template <int MI, int NI>
+template <int MI, int NI, int WN, int ENI, int EWN>
 hipError_t launch_sized(const MmLaunch& a, hipStream_t st) {
   const bool f32 = a.ep.out_f32;
   if (a.a_fmt && a.b_fmt)
-    return f32 ? launch_tile<true, true, true, MI, NI, false, float>(a, st)
-               : launch_tile<true, true, false, MI, NI, false, __bf16>(a, st);
+    return f32 ? launch_tile<true, true, true, MI, ENI, EWN, false, float>(a, st)
+               : launch_tile<true, true, false, MI, NI, WN, false, __bf16>(a, st);
   if (a.a_fmt)
-    return f32 ? launch_tile<true, false, true, MI, NI, false, float>(a, st)
-               : launch_tile<true, false, false, MI, NI, false, __bf16>(a, st);
+    return f32 ? launch_tile<true, false, true, MI, ENI, EWN, false, float>(a, st)
+               : launch_tile<true, false, false, MI, NI, WN, false, __bf16>(a, st);
   if (a.k % 128)
-    return f32 ? launch_tile<false, false, false, MI, NI, true, float>(a, st)
-               : launch_tile<false, false, false, MI, NI, true, __bf16>(a, st);
-  return f32 ? launch_tile<false, false, false, MI, NI, false, float>(a, st)
-             : launch_tile<false, false, false, MI, NI, false, __bf16>(a, st);
+    return f32 ? launch_tile<false, false, false, MI, NI, WN, true, float>(a, st)
+               : launch_tile<false, false, false, MI, NI, WN, true, __bf16>(a, st);
+  return f32 ? launch_tile<false, false, false, MI, NI, WN, false, float>(a, st)
+             : launch_tile<false, false, false, MI, NI, WN, false, __bf16>(a, st);
 }
 
 }  // namespace
 
 hipError_t launch_gemm_tiles(const MmLaunch& a, bool large, hipStream_t st) {
-  return large ? launch_sized<4, 4>(a, st) : launch_sized<2, 2>(a, st);
+  return large ? launch_sized<4, 4, 2, 4, 2>(a, st) : launch_sized<2, 2, 2, 2, 2>(a, st);
 }
 
 }  // namespace mxq
