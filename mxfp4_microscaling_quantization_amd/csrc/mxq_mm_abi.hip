@@ -12,6 +12,7 @@ namespace {
 
 constexpr int64_t kMaxDim = ((int64_t)1 << 31) - 1;  // rows and columns
 constexpr int64_t kMaxK = (int64_t)1 << 22;          // tile-relative byte offsets stay within 32 bits
+constexpr int64_t kMaxLd = (int64_t)1 << 23;         // the same for columns of tokens
 constexpr int64_t kMaxGrid = (int64_t)1 << 30;       // workgroups of one launch, at the smallest tile
 
 bool aligned(const void* p, uintptr_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
@@ -96,30 +97,32 @@ mxq_status mxq_grouped_wgrad(const uint8_t* y, const float* y_scales, int64_t ld
   if (!offsets || !d || (rows > 0 && (!y || !y_scales || !x || !x_scales))) return MXQ_EINVAL;
   if (n == 0 || k == 0 || n > kMaxDim || k > kMaxDim || rows > kMaxDim) return MXQ_ESHAPE;
   if (n > ((int64_t)1 << 40) / k || n * k > ((int64_t)1 << 40) / n_experts) return MXQ_ESHAPE;
-  if (ld_y < rows || ld_x < rows) return MXQ_ESHAPE;
+  if (ld_y < rows || ld_x < rows || ld_y > kMaxLd || ld_x > kMaxLd) return MXQ_ESHAPE;
   if (rows > 0 && (ld_ys < rc_group_slots(rows, n_experts) || ld_xs < rc_group_slots(rows, n_experts)))
     return MXQ_ESHAPE;
   if (((n + 31) / 32) * ((k + 31) / 32) >= kMaxGrid / n_experts) return MXQ_ESHAPE;
   if (ld_y % 16 || ld_x % 16 || !aligned(y, 16) || !aligned(x, 16) || !aligned(y_scales, 4) ||
       !aligned(x_scales, 4) || !aligned(offsets, 8) || !aligned(add, 16) || !aligned(d, 16))
     return MXQ_EALIGN;
-  WgradLaunch l{};
-  l.y = y;
-  l.x = x;
-  l.y_scales = y_scales;
-  l.x_scales = x_scales;
-  l.ld_y = ld_y;
-  l.ld_ys = ld_ys;
-  l.ld_x = ld_x;
-  l.ld_xs = ld_xs;
+  MmLaunch l{};
+  l.a = y;
+  l.b = x;
+  l.a_scales = y_scales;
+  l.b_scales = x_scales;
+  l.a_fmt = l.b_fmt = 1;
   l.rows = rows;
   l.n = n;
   l.k = k;
   l.offsets = offsets;
-  l.experts = (int)n_experts;
-  l.add = add;
-  l.d = d;
-  l.out_f32 = d_dt == MXQ_F32;
+  l.groups = (int)n_experts;
+  l.ld_a = ld_y;
+  l.ld_b = ld_x;
+  l.ld_as = ld_ys;
+  l.ld_bs = ld_xs;
+  l.ep.res = add;
+  l.ep.d = d;
+  l.ep.n = k;
+  l.ep.out_f32 = d_dt == MXQ_F32;
   return from_hip(launch_grouped_wgrad(l, reinterpret_cast<hipStream_t>(stream)));
 }
 

@@ -28,25 +28,18 @@ struct MmLaunch {
   const int64_t* offsets;
   int groups;
   MmEpilogue ep;
+  int64_t ld_a, ld_b, ld_as, ld_bs;  // weight gradient only: row pitches of codes and scales
 };
 
+// Few rows: 16 (few) or 32 rows of a workgroup, the weight straight from memory.
+hipError_t launch_gemm_rows(const MmLaunch& a, bool few, hipStream_t st);
 // The tiled kernel: 256 x 256 results of a workgroup (large) or 128 x 128.
 hipError_t launch_gemm_tiles(const MmLaunch& a, bool large, hipStream_t st);
 hipError_t launch_gemm(const MmLaunch& a, hipStream_t st);
 
-struct WgradLaunch {
-  const uint8_t *y, *x;
-  const float *y_scales, *x_scales;
-  int64_t ld_y, ld_ys, ld_x, ld_xs;
-  int64_t rows, n, k;
-  const int64_t* offsets;
-  int experts;
-  const void* add;
-  void* d;
-  int out_f32;
-};
-
-hipError_t launch_grouped_wgrad(const WgradLaunch& a, hipStream_t st);
+// The weight gradient of every expert: a = dY's FP8 columns [n, ld_a], b = X's [k, ld_b],
+// contracted over the tokens of each segment; ep.d [groups * n, k], ep.n = k.
+hipError_t launch_grouped_wgrad(const MmLaunch& a, hipStream_t st);
 
 struct ActGradLaunch {
   const void *dy, *z;

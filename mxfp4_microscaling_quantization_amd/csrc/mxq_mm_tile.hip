@@ -7,28 +7,30 @@ namespace mxq {
 namespace {
 
 // A workgroup of 2 x WN waves owns 64 MI x 32 NI WN results, a wave 32 MI x 32 NI. The
-// contraction runs in steps of 64 elements, two to a unit of 128. Each operand has a ring
-// of four slots in LDS, 64 bytes of a row in each: a unit of an MXFP4 row or a step of
-// an FP8 row. Direct loads fill the slots three ahead, evenly over the steps: a burst
-// would stall the waves at the memory pipe's door. Fragments of the next step are read
-// from LDS while the matrix cores work on the current one; one barrier a slot (every unit,
-// with FP8 every step) is all that the waves wait for.
-template <bool A8, bool B8, int MI, int NI, int WN>
+// contraction runs in steps of 64 elements, four to a turn of 256. Each operand has R
+// slots in LDS with 128 bytes of every row in each, a whole cache line: a turn of an
+// MXFP4 row or half a turn of an FP8 row. (Direct loads of 1 KiB take 28 cycles as 8 rows
+// of 128 bytes, 36 as 16 rows of 64.) A slot is filled again from the moment when every
+// wave has read its last fragments, the loads spread over the steps. Fragments of the next
+// step are read from LDS while the matrix cores work on the current one; one barrier a
+// slot is all that the waves wait for.
+template <bool A8, bool B8, int MI, int NI, int WN, int R, bool WG>
 struct Tile {
   static constexpr int Waves = 2 * WN, Threads = 64 * Waves;
   static constexpr int BM = 64 * MI, BN = 32 * NI * WN;
-  static constexpr int Ring = 4, ASlot = BM * 64, BSlot = BN * 64;
-  static constexpr int BRing = Ring * ASlot, SRing = BRing + Ring * BSlot;  // offsets in LDS
+  static constexpr int ASlot = BM * 128, BSlot = BN * 128;
+  static constexpr int BRing = R * ASlot, SRing = BRing + R * BSlot;          // offsets in LDS
   static constexpr int DA = ASlot / 1024 / Waves, DB = BSlot / 1024 / Waves;  // 1 KiB loads of a wave for a slot
-  // loads of a step, and those younger than the slot a barrier waits for
-  static constexpr int Issued = (A8 ? DA : DA / 2) + (B8 ? DB : DB / 2);
-  static constexpr int Younger = A8 ? Issued : 3 * Issued;
-  // scales: 16 bytes of a row cover a chunk of four units; two such chunks
-  static constexpr int SRows = BM + BN, SChunk = SRows * 16;
+  // loads of the slots after the one that a barrier waits for (the fewest that are certain)
+  static constexpr int Younger = (R - 2) * (A8 == B8 ? DA + DB : DA);
+  // scales: 16 bytes of a row cover a chunk of two turns; R chunks, loaded R / 2 ahead
+  static constexpr int SRows = BM + BN, SChunk = SRows * 16, Ahead = R / 2;
   static constexpr int SLoads = SRows / 16 / Waves;  // 256-byte loads of a wave in a chunk (16 rows each)
-  static constexpr int Lds = SRing + 2 * SChunk;
+  // weight gradient: a ninth piece of every row, beside each slot
+  static constexpr int XRing = SRing + R * SChunk, XSlot = SRows * 16;
+  static constexpr int Lds = XRing + (WG ? R * XSlot : 0);
   static constexpr int PadN = 32 * NI + 4;  // floats of a row parked for the epilogue
-  static_assert(DA % 2 == 0 && DB % 2 == 0, "half a slot is whole loads");
+  static_assert(DA % 2 == 0 && DB % 2 == 0, "a wave's loads of a slot come in pairs");
   static_assert(Waves * (MI > 2 ? 2 : MI) * 32 * PadN * 4 <= Lds, "the epilogue's rows fit");
 };
 
@@ -43,13 +45,13 @@ __device__ __forceinline__ v4i buffer_of(const void* base, int64_t bytes) {
 // precedes their first reader. (Written in assembly because the compiler would wait
 // for all of them ahead of every LDS read.)
 __device__ __forceinline__ void load_lds16(v4i buf, uint32_t voff, uint32_t soff, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds" ::"s"(lds), "v"(voff),
-               "s"(buf), "s"(soff)
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds" ::"s"(__builtin_amdgcn_readfirstlane(lds)),
+               "v"(voff), "s"(buf), "s"(__builtin_amdgcn_readfirstlane(soff))
                : "memory");
 }
 __device__ __forceinline__ void load_lds4(v4i buf, uint32_t voff, uint32_t soff, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, %3 offen lds" ::"s"(lds), "v"(voff),
-               "s"(buf), "s"(soff)
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, %3 offen lds" ::"s"(__builtin_amdgcn_readfirstlane(lds)),
+               "v"(voff), "s"(buf), "s"(__builtin_amdgcn_readfirstlane(soff))
                : "memory");
 }
 
@@ -63,23 +65,27 @@ __device__ __forceinline__ void barrier() {
 
 // Which 16-byte piece of a row's slot holds logical piece c: rows are spread over the
 // banks so that the reads of a fragment collide in none.
-__device__ __forceinline__ int piece(int row, int c) { return c ^ ((row >> 2) & 3); }
+__device__ __forceinline__ int piece(int row, int c) { return c ^ ((row >> 1) & 7); }
 
 template <bool FP8>
 struct Frag {
   v4i w[FP8 ? 2 : 1];
 };
 
-// This lane's row of a fragment for step s of a unit, from the slot that holds it.
+// Byte offset in a slot of this lane's first piece of the fragment whose first row is 0, and
+// the fragment of step s of a turn: a step's pieces differ from the first step's in whole
+// bits, so one register serves all. (FP8: pieces h and 2 + h, or the lane's 32 elements
+// in order, 2h and 2h + 1, for the exact product.)
 template <bool FP8, bool EXACT>
-__device__ __forceinline__ Frag<FP8> read_frag(const uint8_t* slot, int row, int s, int h) {
+__device__ __forceinline__ int frag_base(int row, int h) {
+  return row * 128 + 16 * piece(row, FP8 && EXACT ? 2 * h : h);
+}
+template <bool FP8, bool EXACT>
+__device__ __forceinline__ Frag<FP8> read_frag(const uint8_t* slot, int base, int i, int s) {
   Frag<FP8> f;
-  if constexpr (FP8) {
-    f.w[0] = *reinterpret_cast<const v4i*>(slot + row * 64 + 16 * piece(row, EXACT ? 2 * h : h));
-    f.w[1] = *reinterpret_cast<const v4i*>(slot + row * 64 + 16 * piece(row, EXACT ? 2 * h + 1 : 2 + h));
-  } else {
-    f.w[0] = *reinterpret_cast<const v4i*>(slot + row * 64 + 16 * piece(row, 2 * s + h));
-  }
+  const int at = base ^ (FP8 ? 64 * (s & 1) : 32 * s);
+  f.w[0] = *reinterpret_cast<const v4i*>(slot + at + 4096 * i);
+  if constexpr (FP8) f.w[1] = *reinterpret_cast<const v4i*>(slot + (at ^ (EXACT ? 16 : 32)) + 4096 * i);
   return f;
 }
 
@@ -99,26 +105,36 @@ __device__ __forceinline__ bf16x8 bf16_of(const Frag<FP8>& f, int j, float scale
     return bf16_from_e2m1((uint32_t)f.w[0][j], scale);
 }
 
-// The scale register of a unit: MXFP4 byte 0 (2) is the block of this lane half in the
-// first (second) step; FP8 byte 0 is the group's exponent.
+// The scale register of two steps: MXFP4 byte 0 (2) is the block of this lane half in the
+// first (second) one; FP8 byte 0 is the group's exponent.
 template <bool FP8>
 __device__ __forceinline__ uint32_t scale_reg(uint32_t raw, int h) {
   return FP8 ? raw >> 23 : raw >> (8 * h);
 }
 
-// One step on the matrix cores, the first (S = 0) or second of a unit. `between` is called MI times in the course of it
+// The byte select of the scale operands is part of the instruction.
+template <bool A8, bool B8>
+__device__ __forceinline__ f32x16 multiply_scaled(const Frag<A8>& a, const Frag<B8>& b, uint32_t sa, uint32_t sb,
+                                                  int step, f32x16 c) {
+  constexpr int FA = A8 ? kE4M3 : kE2M1, FB = B8 ? kE4M3 : kE2M1;
+  if (step == 0)
+    return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(operand_of<B8>(b), operand_of<A8>(a), c, FB, FA, 0, (int)sb,
+                                                           0, (int)sa);
+  return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(operand_of<B8>(b), operand_of<A8>(a), c, FB, FA,
+                                                         B8 ? 0 : 2, (int)sb, A8 ? 0 : 2, (int)sa);
+}
+
+// One step on the matrix cores, the first (step 0) or second of a scale register's two. `between` is called MI times in the course of it
 // (with 0 .. MI - 1) to issue loads while the matrix cores are busy.
-template <bool A8, bool B8, bool EXACT, int MI, int NI, int S, typename F>
+template <bool A8, bool B8, bool EXACT, int MI, int NI, typename F>
 __device__ __forceinline__ void multiply(f32x16 (&c)[MI][NI], const Frag<A8> (&a)[MI], const Frag<B8> (&b)[NI],
-                                         const uint32_t (&sa)[MI], const uint32_t (&sb)[NI], F&& between) {
+                                         const uint32_t (&sa)[MI], const uint32_t (&sb)[NI], int step, F&& between) {
   if constexpr (!EXACT) {
 #pragma unroll
     for (int i = 0; i < MI; ++i) {
 #pragma unroll
       for (int j = 0; j < NI; ++j)
-        c[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
-            operand_of<B8>(b[j]), operand_of<A8>(a[i]), c[i][j], B8 ? kE4M3 : kE2M1, A8 ? kE4M3 : kE2M1,
-            B8 ? 0 : 2 * S, (int)sb[j], A8 ? 0 : 2 * S, (int)sa[i]);
+        c[i][j] = multiply_scaled<A8, B8>(a[i], b[j], sa[i], sb[j], step, c[i][j]);
       __builtin_amdgcn_sched_barrier(0);
       between(i);
       __builtin_amdgcn_sched_barrier(0);
@@ -126,9 +142,9 @@ __device__ __forceinline__ void multiply(f32x16 (&c)[MI][NI], const Frag<A8> (&a
   } else {
     float fa[MI], fb[NI];
 #pragma unroll
-    for (int i = 0; i < MI; ++i) fa[i] = e8m0_operand((A8 ? sa[i] : sa[i] >> (16 * S)) & 255u);
+    for (int i = 0; i < MI; ++i) fa[i] = e8m0_operand((A8 ? sa[i] : sa[i] >> (16 * step)) & 255u);
 #pragma unroll
-    for (int j = 0; j < NI; ++j) fb[j] = e8m0_operand((B8 ? sb[j] : sb[j] >> (16 * S)) & 255u);
+    for (int j = 0; j < NI; ++j) fb[j] = e8m0_operand((B8 ? sb[j] : sb[j] >> (16 * step)) & 255u);
 #pragma unroll
     for (int t = 0; t < 4; ++t) {
       bf16x8 wa[MI];
@@ -153,101 +169,192 @@ __device__ __forceinline__ int xcd_order(int b, int total) {
   return x * q + (x < r ? x : r) + (b >> 3);
 }
 
-template <bool A8, bool B8, bool EXACT, int MI, int NI, int WN, bool ODDK, typename T>
+template <bool A8, bool B8, bool EXACT, int MI, int NI, int WN, int R, bool ODDK, bool WG, typename T>
 __global__ __launch_bounds__(128 * WN, MI *NI > 8 ? 1 : 2) void mm_tile_kernel(MmLaunch p, int col_tiles) {
-  using G = Tile<A8, B8, MI, NI, WN>;
+  using G = Tile<A8, B8, MI, NI, WN, R, WG>;
   extern __shared__ __align__(16) uint8_t lds[];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r = lane & 31, h = lane >> 5;
 
   // the tile
-  const int row_tiles = p.offsets ? segment_tiles(p.offsets, p.groups, p.rows, G::BM)
-                                  : (int)((p.rows + G::BM - 1) / G::BM);
-  const int64_t total = (int64_t)row_tiles * col_tiles;
+  const bool listed = p.offsets && !WG;  // its row tiles are known on the device only
+  const int a_rows = WG ? (int)p.n : 0, b_rows = WG ? (int)p.k : (int)p.n;
+  const int row_tiles = listed ? segment_tiles(p.offsets, p.groups, p.rows, G::BM)
+                        : WG   ? (a_rows + G::BM - 1) / G::BM
+                               : (int)((p.rows + G::BM - 1) / G::BM);
+  const int64_t total = (int64_t)row_tiles * col_tiles * (WG ? p.groups : 1);
   if ((int64_t)blockIdx.x >= total) return;
-  const int at = xcd_order(blockIdx.x, (int)total);
+  int at = xcd_order(blockIdx.x, (int)total);
+  const int group = WG ? at / (row_tiles * col_tiles) : 0;
+  at -= group * row_tiles * col_tiles;
   constexpr int Group = 8;  // row tiles walked together over the columns
   const int band = at / (Group * col_tiles), in_band = at - band * (Group * col_tiles);
   const int tall = row_tiles - band * Group < Group ? row_tiles - band * Group : Group;
   const int row_tile = band * Group + in_band % tall, col_tile = in_band / tall;
   Segment s{0, 0, p.rows, row_tile};
-  if (p.offsets && !find_segment(p.offsets, p.groups, p.rows, G::BM, row_tile, s)) return;
+  if (listed && !find_segment(p.offsets, p.groups, p.rows, G::BM, row_tile, s)) return;
+  // Weight gradient: the contraction runs over the expert's tokens, whose first byte of a
+  // column lies `shift` past a 16-byte boundary.
+  int64_t depth = p.k;
+  int shift = 0, first_slot = 0;
+  if constexpr (WG) {
+    s.expert = group;
+    s.begin = clamp_row(p.offsets[group], p.rows);
+    depth = clamp_row(p.offsets[group + 1], p.rows) - s.begin;
+    depth = depth < 0 ? 0 : depth;
+    shift = (int)(s.begin & 15);
+    first_slot = segment_tiles(p.offsets, group, p.rows, 128);
+  }
 
-  const int64_t abytes = A8 ? p.k : p.k / 2, bbytes = B8 ? p.k : p.k / 2;
-  const int64_t asbytes = A8 ? p.k / 128 * 4 : p.k / 32, bsbytes = B8 ? p.k / 128 * 4 : p.k / 32;
-  const int64_t arow0 = s.begin + (int64_t)s.tile * G::BM;
-  const int64_t brow0 = (int64_t)s.expert * p.n + (int64_t)col_tile * G::BN;
-  const int arows = (int)(s.count - (int64_t)s.tile * G::BM < G::BM ? s.count - (int64_t)s.tile * G::BM : G::BM);
-  const int brows = (int)(p.n - (int64_t)col_tile * G::BN < G::BN ? p.n - (int64_t)col_tile * G::BN : G::BN);
-  const v4i abuf = buffer_of(p.a + arow0 * abytes, arows * abytes);
-  const v4i bbuf = buffer_of(p.b + brow0 * bbytes, brows * bbytes);
+  const int64_t abytes = WG ? p.ld_a : A8 ? p.k : p.k / 2, bbytes = WG ? p.ld_b : B8 ? p.k : p.k / 2;
+  const int64_t asbytes = WG ? 4 * p.ld_as : A8 ? p.k / 128 * 4 : p.k / 32;
+  const int64_t bsbytes = WG ? 4 * p.ld_bs : B8 ? p.k / 128 * 4 : p.k / 32;
+  // first rows and row counts of the operands' tiles; orow0 is the tile's first row of d
+  const int64_t arow0 = WG ? (int64_t)row_tile * G::BM : s.begin + (int64_t)s.tile * G::BM;
+  const int64_t brow0 = (WG ? 0 : (int64_t)s.expert * p.n) + (int64_t)col_tile * G::BN;
+  const int64_t orow0 = WG ? group * p.n + arow0 : arow0;
+  const int64_t aleft = WG ? a_rows - arow0 : s.count - (int64_t)s.tile * G::BM;
+  const int64_t bleft = b_rows - (int64_t)col_tile * G::BN;
+  const int arows = (int)(aleft < G::BM ? aleft : G::BM), brows = (int)(bleft < G::BN ? bleft : G::BN);
+  const int64_t from = WG ? s.begin - shift : 0;  // bytes of a row before the first piece
+  const v4i abuf = buffer_of(p.a + arow0 * abytes + from, arows * abytes - from);
+  const v4i bbuf = buffer_of(p.b + brow0 * bbytes + from, brows * bbytes - from);
   const uint8_t* ascale = static_cast<const uint8_t*>(p.a_scales) + arow0 * asbytes;
   const uint8_t* bscale = static_cast<const uint8_t*>(p.b_scales) + brow0 * bsbytes;
   const v4i asbuf = buffer_of(ascale, arows * asbytes);
   const v4i bsbuf = buffer_of(bscale, brows * bsbytes);
 
-  // byte offsets of this lane's pieces in the slots' loads; rows past the end repeat the last
-  uint32_t va[G::DA], vb[G::DB];
+  // Byte offsets of this lane's pieces in a wave's first two loads of a slot; the others lie
+  // whole rows further on. Rows past the tile's last are past the buffer's end: zeros.
+  uint32_t va[2], vb[2];
 #pragma unroll
-  for (int j = 0; j < G::DA; ++j) {
-    const int row = (wave * G::DA + j) * 16 + lane / 4;
-    va[j] = (uint32_t)((row < arows ? row : arows - 1) * abytes) + 16 * piece(row, lane % 4);
+  for (int j = 0; j < 2; ++j) {
+    const int arow = (wave * G::DA + j) * 8 + lane / 8, brow = (wave * G::DB + j) * 8 + lane / 8;
+    va[j] = (uint32_t)(arow * abytes) + 16 * piece(arow, lane % 8);
+    vb[j] = (uint32_t)(brow * bbytes) + 16 * piece(brow, lane % 8);
   }
-#pragma unroll
-  for (int j = 0; j < G::DB; ++j) {
-    const int row = (wave * G::DB + j) * 16 + lane / 4;
-    vb[j] = (uint32_t)((row < brows ? row : brows - 1) * bbytes) + 16 * piece(row, lane % 4);
-  }
+  const uint32_t apitch = (uint32_t)(16 * abytes), bpitch = (uint32_t)(16 * bbytes);
   const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)lds;
-  const int units = (int)((p.k + 127) / 128);
-  const int tail = (int)(p.k % 128) / 32;  // blocks of the last unit, 0: all four (MXFP4 only: ODDK)
+  const int turns = (int)((depth + 255) / 256);
+  const int halves = (int)(WG ? (depth + 127) / 128 : depth / 128);  // slots of an FP8 operand
+  // blocks of the last turn, 0: all eight
+  const int tail = WG ? 4 * (halves & 1) : (int)(depth % 256) / 32;
+  const int last_steps = tail ? (tail + 1) / 2 : 4;
 
-  // Before the last unit is loaded: pieces past the rows' end repeat the row's first one.
+  // Before the last turn of an MXFP4 operand is loaded: pieces past the rows' end repeat the
+  // row's first one.
   auto trim = [&](int t) {
-    if (ODDK && tail && t == units - 1) {
+    if (tail && t == turns - 1) {
 #pragma unroll
-      for (int j = 0; j < G::DA; ++j) {
-        const int c = piece((wave * G::DA + j) * 16 + lane / 4, lane % 4);
-        va[j] -= c >= tail ? 16 * c : 0;
-      }
-#pragma unroll
-      for (int j = 0; j < G::DB; ++j) {
-        const int c = piece((wave * G::DB + j) * 16 + lane / 4, lane % 4);
-        vb[j] -= c >= tail ? 16 * c : 0;
+      for (int j = 0; j < 2; ++j) {
+        const int ca = piece((wave * G::DA + j) * 8 + lane / 8, lane % 8);
+        const int cb = piece((wave * G::DB + j) * 8 + lane / 8, lane % 8);
+        if (!A8 && ca >= tail) va[j] -= 16 * ca;
+        if (!B8 && cb >= tail) vb[j] -= 16 * cb;
       }
     }
   };
-  // Loads j0 <= j < j1 of slot number q of A (of B): unit q of an MXFP4 operand, step q of an
-  // FP8 one. Past the last slot they load nothing, so that every step has the same number
-  // outstanding.
-  auto load_a = [&](int q, int j0, int j1) {
+  // (Weight gradient: the last group's pieces may pass the end of the last column, so the
+  // offset in the row is part of what the buffer's bounds are checked against.)
+  // Load j of slot number q of A, and of B (q counts turns of an MXFP4 operand, half turns of
+  // an FP8 one). Past the last slot it loads nothing.
+  auto load_a = [&](int q, int j) {
     v4i buf = abuf;
-    buf[2] = q < (A8 ? 2 * units : units) ? buf[2] : 0;
-#pragma unroll
-    for (int j = j0; j < j1; ++j)
-      load_lds16(buf, va[j], (uint32_t)q * 64, lds0 + (q & 3) * G::ASlot + (wave * G::DA + j) * 1024);
+    buf[2] = q < (A8 ? halves : turns) ? buf[2] : 0;
+    const uint32_t at = (uint32_t)q * 128;
+    load_lds16(buf, va[j & 1] + (j >> 1) * apitch + (WG ? at : 0), WG ? 0 : at, lds0 + (q & (R - 1)) * G::ASlot + (wave * G::DA + j) * 1024);
   };
-  auto load_b = [&](int q, int j0, int j1) {
+  auto load_b = [&](int q, int j) {
     v4i buf = bbuf;
-    buf[2] = q < (B8 ? 2 * units : units) ? buf[2] : 0;
-#pragma unroll
-    for (int j = j0; j < j1; ++j)
-      load_lds16(buf, vb[j], (uint32_t)q * 64, lds0 + G::BRing + (q & 3) * G::BSlot + (wave * G::DB + j) * 1024);
+    buf[2] = q < (B8 ? halves : turns) ? buf[2] : 0;
+    const uint32_t at = (uint32_t)q * 128;
+    load_lds16(buf, vb[j & 1] + (j >> 1) * bpitch + (WG ? at : 0), WG ? 0 : at, lds0 + G::BRing + (q & (R - 1)) * G::BSlot + (wave * G::DB + j) * 1024);
   };
-  // Part u of MI of the loads issued in step s of unit t.
+  // Weight gradient. Tokens [0, 128) of a group lie at bytes [shift, 128 + shift) of nine
+  // 16-byte pieces. The first piece's leading bytes, which belong to other tokens, are
+  // replaced by the ninth's when a fragment is read: the sum does not depend on the order
+  // of the tokens, and both operands have the same shift.
+  auto load_ninth = [&](int q) {
+    if (!WG || shift == 0) return;
+#pragma unroll
+    for (int j = wave; j < G::SRows / 64; j += G::Waves) {
+      const bool is_a = j < G::BM / 64;
+      v4i buf = is_a ? abuf : bbuf;
+      buf[2] = q < halves ? buf[2] : 0;
+      const uint32_t row = (is_a ? j : j - G::BM / 64) * 64 + lane;
+      load_lds16(buf, row * (uint32_t)(is_a ? abytes : bbytes) + (uint32_t)q * 128 + 128, 0,
+                 lds0 + G::XRing + (q & (R - 1)) * G::XSlot + j * 1024);
+    }
+  };
+  const uint32_t keep_second = h ? ~0u : 0u;  // the second lane half holds other pieces
+  auto merge_ninth = [&](v4i w, int q, int row) {
+    const v4i x = *reinterpret_cast<const v4i*>(lds + G::XRing + (q & (R - 1)) * G::XSlot + row * 16);
+#pragma unroll
+    for (int d = 0; d < 4; ++d) {
+      const int lead = shift - 4 * d;  // leading bytes of this dword that are replaced
+      const uint32_t own = lead <= 0 ? ~0u : lead >= 4 ? 0u : ~0u << (8 * lead);
+      const uint32_t keep = own | keep_second;
+      w[d] = (int)(((uint32_t)w[d] & keep) | ((uint32_t)x[d] & ~keep));
+    }
+    return w;
+  };
+  // The last group's bytes past its last token become zeros, in both operands.
+  auto clear_group = [&](int q) {
+    const int last = (int)(depth - (int64_t)q * 128);
+    if (last >= 128) return;
+    for (int i = threadIdx.x; i < G::SRows * 9; i += G::Threads) {
+      const int row = i / 9, c = i % 9, keep = last + shift - 16 * c;  // leading bytes that stay
+      if (keep >= 16 || (c == 8 && shift == 0)) continue;
+      const int x = row < G::BM ? row : row - G::BM;
+      uint8_t* slot = row < G::BM ? lds + (q & (R - 1)) * G::ASlot : lds + G::BRing + (q & (R - 1)) * G::BSlot;
+      v4i* at = c == 8 ? reinterpret_cast<v4i*>(lds + G::XRing + (q & (R - 1)) * G::XSlot + row * 16)
+                       : reinterpret_cast<v4i*>(slot + x * 128 + 16 * piece(x, c));
+      v4i w = *at;
+#pragma unroll
+      for (int d = 0; d < 4; ++d) {
+        const int left = keep - 4 * d;
+        w[d] = left >= 4 ? w[d] : left <= 0 ? 0 : (int)((uint32_t)w[d] & ~(~0u << (8 * left)));
+      }
+      *at = w;
+    }
+    wait_loads<0>();
+    barrier();
+  };
+  // The loads issued in step s of turn t, part u of MI of them: those of an FP8 slot in the
+  // odd step that frees it and the step after, those of an MXFP4 slot in the last step and
+  // the first two of the next turn (A's earlier than B's).
   auto load_part = [&](int t, int s, int u) {
-    constexpr int NA = A8 ? G::DA : G::DA / 2, NB = B8 ? G::DB : G::DB / 2;
-    const int a0 = A8 ? 0 : s * NA, b0 = B8 ? 0 : s * NB;
-    load_a(A8 ? 2 * t + s + 3 : t + 3, a0 + u * NA / MI, a0 + (u + 1) * NA / MI);
-    load_b(B8 ? 2 * t + s + 3 : t + 3, b0 + (u * NB + MI - 1) / MI, b0 + ((u + 1) * NB + MI - 1) / MI);
+    if (WG && (s & 1) && u == 0) load_ninth(2 * t + (s + 1) / 2 - 1 + R);
+    if constexpr (A8) {
+#pragma unroll
+      for (int j = 0; j < G::DA; ++j)
+        if ((s & 1) == (j >= G::DA / 2 ? 0 : 1) && j % (G::DA / 2) * MI / (G::DA / 2) == u)
+          load_a(2 * t + (s + 1) / 2 - 1 + R, j);
+    } else {
+#pragma unroll
+      for (int j = 0; j < G::DA; ++j)
+        if (s == (j < 3 ? 3 : 0) && j % 3 % MI == u) load_a(s == 3 ? t + R : t + R - 1, j);
+    }
+    if constexpr (B8) {
+#pragma unroll
+      for (int j = 0; j < G::DB; ++j)
+        if ((s & 1) == (j >= G::DB / 2 ? 0 : 1) && (j % (G::DB / 2) * MI + MI / 2) / (G::DB / 2) == u)
+          load_b(2 * t + (s + 1) / 2 - 1 + R, j);
+    } else {
+#pragma unroll
+      for (int j = 0; j < G::DB; ++j)
+        if (s == (j < 2 ? 0 : 1) && (j + (j < 2)) % MI == u) load_b(t + R - 1, j);
+    }
   };
 
   uint8_t* const sring = lds + G::SRing;
   // Chunk c of the scales: four dwords of every row, by direct loads. A dword past the
   // row's end repeats its last one.
   auto load_scales = [&](int c) {
-    const uint32_t slot = lds0 + G::SRing + (uint32_t)(c & 1) * G::SChunk;
-    const int want = 4 * c + (lane & 3), most = (int)(p.k / 128) - 1, dword = want < most ? want : most;
+    const uint32_t slot = lds0 + G::SRing + (uint32_t)(c & (R - 1)) * G::SChunk;
+    const int want = 4 * c + (lane & 3), most = halves - 1;
+    int dword = first_slot + (want < most ? want : most);
+    if (WG) dword = dword < p.ld_as && dword < p.ld_bs ? dword : 0;  // malformed offsets stay inside
 #pragma unroll
     for (int j = 0; j < G::SLoads; ++j) {
       const int first = (wave * G::SLoads + j) * 16;  // uniform: 16 rows of A or of B
@@ -292,16 +399,16 @@ __global__ __launch_bounds__(128 * WN, MI *NI > 8 ? 1 : 2) void mm_tile_kernel(M
 #pragma unroll
     for (int j = 0; j < SR; ++j) {
       const int row = threadIdx.x + G::Threads * j;
-      if (row < G::SRows) *reinterpret_cast<v4i*>(sring + (c & 1) * G::SChunk + row * 16) = held[j];
+      if (row < G::SRows) *reinterpret_cast<v4i*>(sring + (c & (R - 1)) * G::SChunk + row * 16) = held[j];
     }
   };
-  // The last unit's last step has one block where `tail` is odd: clears the other one.
+  // The last turn's last step has one block where `tail` is odd: clears the other one.
   auto clear_tail = [&]() {
-    uint8_t* a = lds + ((units - 1) & 3) * G::ASlot;
-    uint8_t* b = lds + G::BRing + ((units - 1) & 3) * G::BSlot;
+    uint8_t* a = lds + ((turns - 1) & (R - 1)) * G::ASlot;
+    uint8_t* b = lds + G::BRing + ((turns - 1) & (R - 1)) * G::BSlot;
     for (int row = threadIdx.x; row < G::SRows; row += G::Threads) {
       const int x = row < G::BM ? row : row - G::BM;
-      *reinterpret_cast<v4i*>((row < G::BM ? a : b) + x * 64 + 16 * piece(x, tail)) = v4i{0, 0, 0, 0};
+      *reinterpret_cast<v4i*>((row < G::BM ? a : b) + x * 128 + 16 * piece(x, tail)) = v4i{0, 0, 0, 0};
     }
     wait_loads<0>();
     barrier();
@@ -309,22 +416,50 @@ __global__ __launch_bounds__(128 * WN, MI *NI > 8 ? 1 : 2) void mm_tile_kernel(M
 
   const int wm = wave / WN, wn = wave % WN;
   const int arow = wm * 32 * MI + r, brow = wn * 32 * NI + r;
-  Frag<A8> fa[2][MI];
+  int abase = frag_base<A8, EXACT>(arow, h), bbase = frag_base<B8, EXACT>(brow, h);
+  // Two FP8 fragment sets of A do not fit the registers: a fragment is then replaced by the
+  // next step's as soon as its last product is issued.
+  constexpr bool Roll = A8 && B8 && !EXACT;
+  Frag<A8> fa[Roll ? 1 : 2][MI];
   Frag<B8> fb[2][NI];
   uint32_t sa[MI], sb[NI], ra[MI], rb[NI];
   f32x16 c[MI][NI] = {};
-
-  auto read_step = [&](int t, int s, Frag<A8>(&xa)[MI], Frag<B8>(&xb)[NI]) {
-    const uint8_t* a = lds + ((A8 ? 2 * t + s : t) & 3) * G::ASlot;
-    const uint8_t* b = lds + G::BRing + ((B8 ? 2 * t + s : t) & 3) * G::BSlot;
+  // The sums pass through an empty statement after every step: the products, which have
+  // no side effects, would else sink below the barriers and keep every fragment alive.
+  auto pin = [&]() {
 #pragma unroll
-    for (int i = 0; i < MI; ++i) xa[i] = read_frag<A8, EXACT>(a, arow + 32 * i, s, h);
+    for (int i = 0; i < MI; ++i)
 #pragma unroll
-    for (int j = 0; j < NI; ++j) xb[j] = read_frag<B8, EXACT>(b, brow + 32 * j, s, h);
+      for (int j = 0; j < NI; ++j) {
+        if constexpr (MI * NI > 8)
+          asm volatile("" : "+a"(c[i][j]));
+        else
+          asm volatile("" : "+v"(c[i][j]));
+      }
   };
-  // The scales of unit t as they lie in LDS; select_scales makes them the instructions'.
-  auto read_scales = [&](int t) {
-    const uint8_t* q = sring + ((t >> 2) & 1) * G::SChunk + 4 * (t & 3);
+  auto read_a = [&](int t, int s, int i) {
+    Frag<A8> f = read_frag<A8, EXACT>(lds + ((A8 ? 2 * t + (s >> 1) : t) & (R - 1)) * G::ASlot, abase, i, s);
+    if (WG && (s & 1) == 0) f.w[0] = merge_ninth(f.w[0], 2 * t + (s >> 1), arow + 32 * i);
+    return f;
+  };
+  // Fragments of step s of turn t: B's, and A's where they are not replaced one by one.
+  auto read_step = [&](int t, int s) {
+    const uint8_t* b = lds + G::BRing + ((B8 ? 2 * t + (s >> 1) : t) & (R - 1)) * G::BSlot;
+    if constexpr (!Roll) {
+#pragma unroll
+      for (int i = 0; i < MI; ++i) fa[s & 1][i] = read_a(t, s, i);
+    }
+#pragma unroll
+    for (int j = 0; j < NI; ++j) {
+      fb[s & 1][j] = read_frag<B8, EXACT>(b, bbase, j, s);
+      if (WG && (s & 1) == 0)
+        fb[s & 1][j].w[0] = merge_ninth(fb[s & 1][j].w[0], 2 * t + (s >> 1), G::BM + brow + 32 * j);
+    }
+  };
+  // The scales of steps 2u and 2u + 1 as they lie in LDS; select_scales makes them the
+  // instructions'.
+  auto read_scales = [&](int u) {
+    const uint8_t* q = sring + ((u >> 2) & (R - 1)) * G::SChunk + 4 * (u & 3);
 #pragma unroll
     for (int i = 0; i < MI; ++i) ra[i] = *reinterpret_cast<const uint32_t*>(q + 16 * (arow + 32 * i));
 #pragma unroll
@@ -336,65 +471,102 @@ __global__ __launch_bounds__(128 * WN, MI *NI > 8 ? 1 : 2) void mm_tile_kernel(M
 #pragma unroll
     for (int j = 0; j < NI; ++j) sb[j] = scale_reg<B8>(rb[j], h);
   };
-  auto idle = [](int) {};
 
+  if (!WG || turns > 0) {
   if constexpr (ODDK) {
     fetch_scales(0);
     park_scales(0);
   } else {
-    load_scales(0);
-  }
 #pragma unroll
-  for (int q = 0; q < 3; ++q) {
-    trim(q);
-    load_a(q, 0, G::DA);
-    load_b(q, 0, G::DB);
+    for (int c = 0; c < G::Ahead; ++c)
+      if (c == 0 || 2 * c < turns) load_scales(c);
   }
-  wait_loads<2 * (G::DA + G::DB)>();
+  // the slots, of the last ones only what the steps to come do not load
+#pragma unroll
+  for (int q = 0; q < R; ++q) {
+    trim(q);
+    load_ninth(q);
+#pragma unroll
+    for (int j = 0; j < (q < R - 1 ? G::DA : A8 ? G::DA / 2 : G::DA < 3 ? G::DA : 3); ++j) load_a(q, j);
+#pragma unroll
+    for (int j = 0; j < (q < R - 1 ? G::DB : B8 ? G::DB / 2 : 0); ++j) load_b(q, j);
+  }
+  constexpr int Now = (A8 ? G::DA / 2 : G::DA < 3 ? G::DA : 3) + (B8 ? G::DB / 2 : 0);
+  wait_loads<Now + (R - 2) * (G::DA + G::DB)>();
   barrier();
-  if (ODDK && (tail & 1) && units == 1) clear_tail();
-  read_step(0, 0, fa[0], fb[0]);
+  if (ODDK && (tail & 1) && turns == 1) clear_tail();
+  if (WG && halves == 1) clear_group(0);
+  read_step(0, 0);
+  if constexpr (Roll) {
+#pragma unroll
+    for (int i = 0; i < MI; ++i) fa[0][i] = read_a(0, 0, i);
+  }
   read_scales(0);
   select_scales();
 
-  for (int t = 0; t + 1 < units; ++t) {
-    // first step
-    if constexpr (A8) {
+  for (int t = 0; t + 1 < turns; ++t) {
+    asm volatile("" : "+v"(abase), "+v"(bbase));  // addresses are formed where used, not held
+    if constexpr (ODDK) {
+      // chunk c + 1 is fetched in the first turn of chunk c and parked in the second
+      if ((t & 1) == 0 && t + 2 < turns) fetch_scales((t >> 1) + 1);
+      if ((t & 1) == 1 && t + 1 < turns) park_scales((t >> 1) + 1);
+    }
+#pragma unroll
+    for (int s = 0; s < 4; ++s) {
+      // the next slots have landed, and every wave has its last fragments of the current ones
+      if (s == 3 || (s == 1 && (A8 || B8))) {
+        wait_loads<G::Younger>();
+        barrier();
+        if (WG && s == 3 && t + 2 == turns && (halves & 1)) clear_group(halves - 1);
+      }
+      if (s == 3) {
+        if (ODDK && (tail & 1) && t + 2 == turns) clear_tail();
+        trim(t + R);
+        if constexpr (!ODDK)
+          if ((t & 1) == 0 && t + 2 * G::Ahead < turns) load_scales((t >> 1) + G::Ahead);
+      }
+      const int tn = s == 3 ? t + 1 : t, sn = (s + 1) & 3;
+      read_step(tn, sn);
+      if (s & 1) read_scales(2 * t + (s + 1) / 2);
+      __builtin_amdgcn_sched_barrier(0);
+      multiply<A8, B8, EXACT, MI, NI>(c, fa[Roll ? 0 : s & 1], fb[s & 1], sa, sb, s & 1, [&](int u) {
+        if constexpr (Roll) fa[0][u] = read_a(tn, sn, u);
+        load_part(t, s, u);
+      });
+      pin();
+      __builtin_amdgcn_sched_barrier(0);
+      if (s & 1) select_scales();
+    }
+  }
+  // the last turn: one to four steps (two or four where k is a multiple of 128)
+  auto finish = [&](int s) {
+    if (s + 1 < last_steps) {
+      read_step(turns - 1, s + 1);
+      if (s == 1) read_scales(2 * turns - 1);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+    multiply<A8, B8, EXACT, MI, NI>(c, fa[Roll ? 0 : s & 1], fb[s & 1], sa, sb, s & 1, [&](int u) {
+      if constexpr (Roll)
+        if (s + 1 < last_steps) fa[0][u] = read_a(turns - 1, s + 1, u);
+      if (s == 0) load_part(turns - 1, 0, u);
+    });
+    pin();
+    if (s == 1) select_scales();
+  };
+  finish(0);
+  if (!ODDK || last_steps > 1) {
+    if constexpr (A8 || B8) {
       wait_loads<G::Younger>();
       barrier();
+      if (WG && 2 * turns == halves) clear_group(halves - 1);
     }
-    trim(t + 3);
-    if constexpr (ODDK) {
-      // chunk c + 1 is fetched in the first unit of chunk c and parked in the third
-      if ((t & 3) == 0 && t + 4 < units) fetch_scales((t >> 2) + 1);
-      if ((t & 3) == 2 && t + 2 < units) park_scales((t >> 2) + 1);
-    } else {
-      if ((t & 3) == 0 && t + 4 < units) load_scales((t >> 2) + 1);
+    finish(1);
+    if (last_steps > 2) {
+      finish(2);
+      if (!ODDK || last_steps > 3) finish(3);
     }
-    read_step(t, 1, fa[1], fb[1]);
-    __builtin_amdgcn_sched_barrier(0);
-    multiply<A8, B8, EXACT, MI, NI, 0>(c, fa[0], fb[0], sa, sb, [&](int u) { load_part(t, 0, u); });
-    __builtin_amdgcn_sched_barrier(0);
-    // second step: the next slots have landed once at most the younger loads are outstanding,
-    // and every wave has read its last fragments of the slots that are filled next
-    wait_loads<G::Younger>();
-    barrier();
-    if (ODDK && (tail & 1) && t + 2 == units) clear_tail();
-    read_step(t + 1, 0, fa[0], fb[0]);
-    read_scales(t + 1);
-    __builtin_amdgcn_sched_barrier(0);
-    multiply<A8, B8, EXACT, MI, NI, 1>(c, fa[1], fb[1], sa, sb, [&](int u) { load_part(t, 1, u); });
-    __builtin_amdgcn_sched_barrier(0);
-    select_scales();
   }
-  if constexpr (A8) {
-    wait_loads<G::Younger>();
-    barrier();
   }
-  const bool both = !ODDK || tail == 0 || tail > 2;
-  if (both) read_step(units - 1, 1, fa[1], fb[1]);
-  multiply<A8, B8, EXACT, MI, NI, 0>(c, fa[0], fb[0], sa, sb, idle);
-  if (both) multiply<A8, B8, EXACT, MI, NI, 1>(c, fa[1], fb[1], sa, sb, idle);
 
   // Epilogue: a block of rows at a time through LDS, so that rows leave as whole runs.
   wait_loads<0>();
@@ -420,19 +592,20 @@ __global__ __launch_bounds__(128 * WN, MI *NI > 8 ? 1 : 2) void mm_tile_kernel(M
     }
     __builtin_amdgcn_wave_barrier();
     const int first = wm * 32 * MI + block * Park * 32 + prow;
-    out.rows(p.ep, park + prow * G::PadN + pcol, RowsAtOnce * G::PadN, arow0 + first, arows - first, RowsAtOnce,
+    out.rows(p.ep, park + prow * G::PadN + pcol, RowsAtOnce * G::PadN, orow0 + first, arows - first, RowsAtOnce,
              Park * 32 / RowsAtOnce);
     __builtin_amdgcn_wave_barrier();
   }
 }
 
-template <bool A8, bool B8, bool EXACT, int MI, int NI, int WN, bool ODDK, typename T>
+template <bool A8, bool B8, bool EXACT, int MI, int NI, int WN, int R, bool ODDK, bool WG, typename T>
 hipError_t launch_tile(const MmLaunch& a, hipStream_t st) {
-  using G = Tile<A8, B8, MI, NI, WN>;
-  const int64_t col_tiles = (a.n + G::BN - 1) / G::BN;
-  const int64_t row_tiles = a.offsets ? a.rows / G::BM + (a.rows < a.groups ? a.rows : a.groups)
-                                      : (a.rows + G::BM - 1) / G::BM;
-  auto k = mm_tile_kernel<A8, B8, EXACT, MI, NI, WN, ODDK, T>;
+  using G = Tile<A8, B8, MI, NI, WN, R, WG>;
+  const int64_t col_tiles = ((WG ? a.k : a.n) + G::BN - 1) / G::BN;
+  const int64_t row_tiles = WG          ? (a.n + G::BM - 1) / G::BM * a.groups
+                            : a.offsets ? a.rows / G::BM + (a.rows < a.groups ? a.rows : a.groups)
+                                        : (a.rows + G::BM - 1) / G::BM;
+  auto k = mm_tile_kernel<A8, B8, EXACT, MI, NI, WN, R, ODDK, WG, T>;
   static const hipError_t set =
       hipFuncSetAttribute(reinterpret_cast<const void*>(k), hipFuncAttributeMaxDynamicSharedMemorySize, G::Lds);
   if (set != hipSuccess) return set;
@@ -440,26 +613,37 @@ hipError_t launch_tile(const MmLaunch& a, hipStream_t st) {
   return hipGetLastError();
 }
 
-template <int MI, int NI, int WN, int ENI, int EWN>
+// Waves of 32 MI x 32 NI results, WN of them across; the exact product's need the registers
+// of a wave that has a SIMD for itself in the large tile (ENI, EWN).
+template <int MI, int NI, int WN, int ENI, int EWN, int R>
 hipError_t launch_sized(const MmLaunch& a, hipStream_t st) {
   const bool f32 = a.ep.out_f32;
   if (a.a_fmt && a.b_fmt)
-    return f32 ? launch_tile<true, true, true, MI, ENI, EWN, false, float>(a, st)
-               : launch_tile<true, true, false, MI, NI, WN, false, __bf16>(a, st);
+    return f32 ? launch_tile<true, true, true, MI, ENI, EWN, R, false, false, float>(a, st)
+               : launch_tile<true, true, false, MI, NI, WN, R, false, false, __bf16>(a, st);
   if (a.a_fmt)
-    return f32 ? launch_tile<true, false, true, MI, ENI, EWN, false, float>(a, st)
-               : launch_tile<true, false, false, MI, NI, WN, false, __bf16>(a, st);
+    return f32 ? launch_tile<true, false, true, MI, ENI, EWN, R, false, false, float>(a, st)
+               : launch_tile<true, false, false, MI, NI, WN, R, false, false, __bf16>(a, st);
   if (a.k % 128)
-    return f32 ? launch_tile<false, false, false, MI, NI, WN, true, float>(a, st)
-               : launch_tile<false, false, false, MI, NI, WN, true, __bf16>(a, st);
-  return f32 ? launch_tile<false, false, false, MI, NI, WN, false, float>(a, st)
-             : launch_tile<false, false, false, MI, NI, WN, false, __bf16>(a, st);
+    return f32 ? launch_tile<false, false, false, MI, NI, WN, R, true, false, float>(a, st)
+               : launch_tile<false, false, false, MI, NI, WN, R, true, false, __bf16>(a, st);
+  return f32 ? launch_tile<false, false, false, MI, NI, WN, R, false, false, float>(a, st)
+             : launch_tile<false, false, false, MI, NI, WN, R, false, false, __bf16>(a, st);
 }
 
 }  // namespace
 
 hipError_t launch_gemm_tiles(const MmLaunch& a, bool large, hipStream_t st) {
-  return large ? launch_sized<4, 4, 2, 4, 2>(a, st) : launch_sized<2, 2, 2, 2, 2>(a, st);
+  return large ? launch_sized<4, 2, 4, 4, 2, 2>(a, st) : launch_sized<2, 1, 4, 1, 4, 4>(a, st);
+}
+
+hipError_t launch_grouped_wgrad(const MmLaunch& a, hipStream_t st) {
+  const bool large = a.n > 128 && a.k > 128;
+  if (large)
+    return a.ep.out_f32 ? launch_tile<true, true, true, 4, 4, 2, 2, false, true, float>(a, st)
+                        : launch_tile<true, true, false, 4, 2, 4, 2, false, true, __bf16>(a, st);
+  return a.ep.out_f32 ? launch_tile<true, true, true, 2, 1, 4, 4, false, true, float>(a, st)
+                      : launch_tile<true, true, false, 2, 1, 4, 4, false, true, __bf16>(a, st);
 }
 
 }  // namespace mxq

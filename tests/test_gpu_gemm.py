@@ -103,6 +103,16 @@ def test_grouped(counts, fmt):
     check_product(2, counts, 270, 256, fmt, "swiglu", torch.float32, True, True, torch.float32)
 
 
+@pytest.mark.parametrize("fmt,k,dtype", [("44", 640, torch.bfloat16), ("44", 512, torch.float32), ("44", 160, torch.bfloat16),
+                                         ("44", 96, torch.float32), ("84", 384, torch.bfloat16),
+                                         ("84", 256, torch.float32), ("88", 384, torch.bfloat16),
+                                         ("88", 1152, torch.bfloat16), ("88", 640, torch.float32)])
+def test_many_tiles(fmt, k, dtype):
+    """Sizes that take the 256 x 256 tiles, ragged on both sides; then tokens of experts."""
+    check_product(k, [4130], 4100, k, fmt, "gelu", torch.float32, True, True, dtype, grouped=False)
+    check_product(k, [2000, 0, 1030, 257, 900], 4160, k, fmt, "swiglu", torch.bfloat16, False, True, dtype)
+
+
 def test_grouped_many_experts():
     rng = np.random.default_rng(5)
     counts = rng.integers(0, 4, 1500).tolist()
