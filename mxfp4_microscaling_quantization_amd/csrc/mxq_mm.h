@@ -46,13 +46,17 @@ __device__ __forceinline__ bf16x8 bf16_from_e2m1(uint32_t w, float scale) {
 // ---------------------------------------------------------------------------
 // Activations and their derivatives in fp32. exp and the reciprocal are the hardware's
 // (about 1e-7 relative).
+constexpr float kLog2e = 1.4426950408889634f;
 __device__ __forceinline__ float sigmoid_f(float z) {
-  return __builtin_amdgcn_rcpf(1.0f + __expf(-z));
+  return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-kLog2e * z));
 }
 constexpr float kGeluA = 1.5957691216057308f;          // 2 sqrt(2/pi)
 constexpr float kGeluB = 1.5957691216057308f * 0.044715f;
 // tanh(u) = 2 sigmoid(2u) - 1, so the tanh form of GELU is z sigmoid(2u).
-__device__ __forceinline__ float gelu_f(float z) { return z * sigmoid_f(z * fmaf(kGeluB * z, z, kGeluA)); }
+__device__ __forceinline__ float gelu_f(float z) {
+  const float w = z * fmaf(-kLog2e * kGeluB, z * z, -kLog2e * kGeluA);
+  return z * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(w));
+}
 
 __device__ __forceinline__ float act_f(float z, int act) {
   switch (act) {

@@ -80,6 +80,7 @@ template <bool FP8, bool EXACT>
 __device__ __forceinline__ int frag_base(int row, int h) {
   return row * 128 + 16 * piece(row, FP8 && EXACT ? 2 * h : h);
 }
+__device__ __forceinline__ int row16(int base) { return (base >> 7) * 16; }  // 16 times its row
 template <bool FP8, bool EXACT>
 __device__ __forceinline__ Frag<FP8> read_frag(const uint8_t* slot, int base, int i, int s) {
   Frag<FP8> f;
@@ -184,9 +185,11 @@ __global__ __launch_bounds__(128 * WN, MI *NI > 8 ? 1 : 2) void mm_tile_kernel(M
                                : (int)((p.rows + G::BM - 1) / G::BM);
   const int64_t total = (int64_t)row_tiles * col_tiles * (WG ? p.groups : 1);
   if ((int64_t)blockIdx.x >= total) return;
-  int at = xcd_order(blockIdx.x, (int)total);
-  const int group = WG ? at / (row_tiles * col_tiles) : 0;
-  at -= group * row_tiles * col_tiles;
+  // Weight gradient: the experts one after the other, each over all XCDs, for their tiles
+  // cost what they have tokens.
+  const int listed_tiles = WG ? row_tiles * col_tiles : (int)total;
+  const int group = WG ? blockIdx.x / listed_tiles : 0;
+  const int at = xcd_order(blockIdx.x - group * listed_tiles, listed_tiles);
   constexpr int Group = 8;  // row tiles walked together over the columns
   const int band = at / (Group * col_tiles), in_band = at - band * (Group * col_tiles);
   const int tall = row_tiles - band * Group < Group ? row_tiles - band * Group : Group;
@@ -245,10 +248,12 @@ __global__ __launch_bounds__(128 * WN, MI *NI > 8 ? 1 : 2) void mm_tile_kernel(M
   // row's first one.
   auto trim = [&](int t) {
     if (tail && t == turns - 1) {
+      int l = lane;
+      asm volatile("" : "+v"(l));
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        const int ca = piece((wave * G::DA + j) * 8 + lane / 8, lane % 8);
-        const int cb = piece((wave * G::DB + j) * 8 + lane / 8, lane % 8);
+        const int ca = piece((wave * G::DA + j) * 8 + l / 8, l % 8);
+        const int cb = piece((wave * G::DB + j) * 8 + l / 8, l % 8);
         if (!A8 && ca >= tail) va[j] -= 16 * ca;
         if (!B8 && cb >= tail) vb[j] -= 16 * cb;
       }
@@ -276,19 +281,21 @@ __global__ __launch_bounds__(128 * WN, MI *NI > 8 ? 1 : 2) void mm_tile_kernel(M
   // of the tokens, and both operands have the same shift.
   auto load_ninth = [&](int q) {
     if (!WG || shift == 0) return;
+    int l = lane;
+    asm volatile("" : "+v"(l));  // (addresses formed here, not held over the turns)
 #pragma unroll
     for (int j = wave; j < G::SRows / 64; j += G::Waves) {
       const bool is_a = j < G::BM / 64;
       v4i buf = is_a ? abuf : bbuf;
       buf[2] = q < halves ? buf[2] : 0;
-      const uint32_t row = (is_a ? j : j - G::BM / 64) * 64 + lane;
+      const uint32_t row = (is_a ? j : j - G::BM / 64) * 64 + l;
       load_lds16(buf, row * (uint32_t)(is_a ? abytes : bbytes) + (uint32_t)q * 128 + 128, 0,
                  lds0 + G::XRing + (q & (R - 1)) * G::XSlot + j * 1024);
     }
   };
-  const uint32_t keep_second = h ? ~0u : 0u;  // the second lane half holds other pieces
-  auto merge_ninth = [&](v4i w, int q, int row) {
-    const v4i x = *reinterpret_cast<const v4i*>(lds + G::XRing + (q & (R - 1)) * G::XSlot + row * 16);
+  uint32_t keep_second = h ? ~0u : 0u;  // the second lane half holds other pieces
+  auto merge_ninth = [&](v4i w, int q, int at) {
+    const v4i x = *reinterpret_cast<const v4i*>(lds + G::XRing + (q & (R - 1)) * G::XSlot + at);
 #pragma unroll
     for (int d = 0; d < 4; ++d) {
       const int lead = shift - 4 * d;  // leading bytes of this dword that are replaced
@@ -352,13 +359,15 @@ __global__ __launch_bounds__(128 * WN, MI *NI > 8 ? 1 : 2) void mm_tile_kernel(M
   // row's end repeats its last one.
   auto load_scales = [&](int c) {
     const uint32_t slot = lds0 + G::SRing + (uint32_t)(c & (R - 1)) * G::SChunk;
-    const int want = 4 * c + (lane & 3), most = halves - 1;
+    int l = lane;
+    asm volatile("" : "+v"(l));  // (addresses formed here, not held over the turns)
+    const int want = 4 * c + (l & 3), most = halves - 1;
     int dword = first_slot + (want < most ? want : most);
     if (WG) dword = dword < p.ld_as && dword < p.ld_bs ? dword : 0;  // malformed offsets stay inside
 #pragma unroll
     for (int j = 0; j < G::SLoads; ++j) {
       const int first = (wave * G::SLoads + j) * 16;  // uniform: 16 rows of A or of B
-      const int row = first + (lane >> 2);
+      const int row = first + (l >> 2);
       if (first < G::BM)
         load_lds4(asbuf, (uint32_t)((row < arows ? row : arows - 1) * asbytes) + 4 * dword, 0, slot + first * 16);
       else
@@ -439,7 +448,7 @@ __global__ __launch_bounds__(128 * WN, MI *NI > 8 ? 1 : 2) void mm_tile_kernel(M
   };
   auto read_a = [&](int t, int s, int i) {
     Frag<A8> f = read_frag<A8, EXACT>(lds + ((A8 ? 2 * t + (s >> 1) : t) & (R - 1)) * G::ASlot, abase, i, s);
-    if (WG && (s & 1) == 0) f.w[0] = merge_ninth(f.w[0], 2 * t + (s >> 1), arow + 32 * i);
+    if (WG && (s & 1) == 0) f.w[0] = merge_ninth(f.w[0], 2 * t + (s >> 1), row16(abase) + 512 * i);
     return f;
   };
   // Fragments of step s of turn t: B's, and A's where they are not replaced one by one.
@@ -453,7 +462,7 @@ __global__ __launch_bounds__(128 * WN, MI *NI > 8 ? 1 : 2) void mm_tile_kernel(M
     for (int j = 0; j < NI; ++j) {
       fb[s & 1][j] = read_frag<B8, EXACT>(b, bbase, j, s);
       if (WG && (s & 1) == 0)
-        fb[s & 1][j].w[0] = merge_ninth(fb[s & 1][j].w[0], 2 * t + (s >> 1), G::BM + brow + 32 * j);
+        fb[s & 1][j].w[0] = merge_ninth(fb[s & 1][j].w[0], 2 * t + (s >> 1), 16 * G::BM + row16(bbase) + 512 * j);
     }
   };
   // The scales of steps 2u and 2u + 1 as they lie in LDS; select_scales makes them the
@@ -461,9 +470,9 @@ __global__ __launch_bounds__(128 * WN, MI *NI > 8 ? 1 : 2) void mm_tile_kernel(M
   auto read_scales = [&](int u) {
     const uint8_t* q = sring + ((u >> 2) & (R - 1)) * G::SChunk + 4 * (u & 3);
 #pragma unroll
-    for (int i = 0; i < MI; ++i) ra[i] = *reinterpret_cast<const uint32_t*>(q + 16 * (arow + 32 * i));
+    for (int i = 0; i < MI; ++i) ra[i] = *reinterpret_cast<const uint32_t*>(q + row16(abase) + 512 * i);
 #pragma unroll
-    for (int j = 0; j < NI; ++j) rb[j] = *reinterpret_cast<const uint32_t*>(q + 16 * (G::BM + brow + 32 * j));
+    for (int j = 0; j < NI; ++j) rb[j] = *reinterpret_cast<const uint32_t*>(q + 16 * G::BM + row16(bbase) + 512 * j);
   };
   auto select_scales = [&]() {
 #pragma unroll
@@ -505,7 +514,9 @@ __global__ __launch_bounds__(128 * WN, MI *NI > 8 ? 1 : 2) void mm_tile_kernel(M
   select_scales();
 
   for (int t = 0; t + 1 < turns; ++t) {
-    asm volatile("" : "+v"(abase), "+v"(bbase));  // addresses are formed where used, not held
+    // addresses and masks are formed where used, not held
+    asm volatile("" : "+v"(abase), "+v"(bbase));
+    if constexpr (WG) asm volatile("" : "+v"(keep_second));
     if constexpr (ODDK) {
       // chunk c + 1 is fetched in the first turn of chunk c and parked in the second
       if ((t & 1) == 0 && t + 2 < turns) fetch_scales((t >> 1) + 1);
