@@ -176,27 +176,24 @@ struct RunEpilogue {
     }
   }
 
-  // Rows row, row + step, ... (count of them, those from `rows` on missing), their sums at
-  // z, z + zstep, ...
-  __device__ __forceinline__ void rows(const MmEpilogue& ep, const float* z, int zstep, int64_t row, int rows, int step,
-                                       int count) {
-    constexpr int U = 4;
+  // N rows `row`, row + STEP, ... (those from `rows` on missing), whose sums get(k, z) fetches.
+  template <int N, int STEP, typename F>
+  __device__ __forceinline__ void rows(const MmEpilogue& ep, F&& get, int64_t row, int rows) {
+    constexpr int U = N < 4 ? N : 4;
     if (left <= 0) return;
     T* d = static_cast<T*>(ep.d) + row * dn + dcol;
     const T* res = static_cast<const T*>(ep.res) + row * dn + dcol;
     T* keep = static_cast<T*>(ep.z) + row * ep.n + n0;
-    const int64_t dstep = step * dn, kstep = step * ep.n;
+    const int64_t dstep = STEP * dn, kstep = STEP * ep.n;
 #pragma unroll 1
-    for (int u = 0; u < count; u += U) {
+    for (int u = 0; u < N; u += U) {
       float v[U][V], r[U][V];
 #pragma unroll
-      for (int k = 0; k < U; ++k)
-#pragma unroll
-        for (int i = 0; i < V; ++i) v[k][i] = z[k * zstep + i];
+      for (int k = 0; k < U; ++k) get(u + k, v[k]);
       if (ep.res && vec) {
 #pragma unroll
         for (int k = 0; k < U; ++k) {
-          if ((u + k) * step < rows) {
+          if ((u + k) * STEP < rows) {
             if (gated) {
               float half[V / 2];
               get_run<T, V / 2>(res + k * dstep, half);
@@ -217,7 +214,7 @@ struct RunEpilogue {
       if (ep.z) {
 #pragma unroll
         for (int k = 0; k < U; ++k)
-          if ((u + k) * step < rows) store_run<T, V>(keep + k * kstep, nullptr, v[k], left, vec);
+          if ((u + k) * STEP < rows) store_run<T, V>(keep + k * kstep, nullptr, v[k], left, vec);
       }
       if (gated) {
 #pragma unroll
@@ -228,7 +225,7 @@ struct RunEpilogue {
             g[i] = v[k][2 * i] * sigmoid_f(v[k][2 * i]) * v[k][2 * i + 1];
             if (ep.res && vec) g[i] += r[k][i];
           }
-          if ((u + k) * step < rows)
+          if ((u + k) * STEP < rows)
             store_run<T, V / 2>(d + k * dstep, vec || !ep.res ? nullptr : res + k * dstep, g, left / 2, vec);
         }
       } else {
@@ -239,11 +236,10 @@ struct RunEpilogue {
 #pragma unroll
             for (int i = 0; i < V; ++i) v[k][i] += r[k][i];
           }
-          if ((u + k) * step < rows)
+          if ((u + k) * STEP < rows)
             store_run<T, V>(d + k * dstep, vec || !ep.res ? nullptr : res + k * dstep, v[k], left, vec);
         }
       }
-      z += U * zstep;
       d += U * dstep;
       res += U * dstep;
       keep += U * kstep;

@@ -6,6 +6,8 @@ namespace mxq {
 
 namespace {
 
+constexpr int kCUs = 256;  // of an MI355X; the tiles' LDS leaves room for one workgroup of each
+
 // A workgroup of 2 x WN waves owns 64 MI x 32 NI WN results, a wave 32 MI x 32 NI. The
 // contraction runs in steps of 64 elements, four to a turn of 256. Each operand has R
 // slots in LDS with 128 bytes of every row in each, a whole cache line: a turn of an
@@ -19,7 +21,7 @@ struct Tile {
   static constexpr int Waves = 2 * WN, Threads = 64 * Waves;
   static constexpr int BM = 64 * MI, BN = 32 * NI * WN;
   static constexpr int ASlot = BM * 128, BSlot = BN * 128;
-  static constexpr int BRing = R * ASlot, SRing = BRing + R * BSlot;          // offsets in LDS
+  static constexpr int Slot = ASlot + BSlot, SRing = R * Slot;                // offsets in LDS
   static constexpr int DA = ASlot / 1024 / Waves, DB = BSlot / 1024 / Waves;  // 1 KiB loads of a wave for a slot
   // loads of the slots after the one that a barrier waits for (the fewest that are certain)
   static constexpr int Younger = (R - 2) * (A8 == B8 ? DA + DB : DA);
@@ -29,9 +31,10 @@ struct Tile {
   // weight gradient: a ninth piece of every row, beside each slot
   static constexpr int XRing = SRing + R * SChunk, XSlot = SRows * 16;
   static constexpr int Lds = XRing + (WG ? R * XSlot : 0);
-  static constexpr int PadN = 32 * NI + 4;  // floats of a row parked for the epilogue
+  // 32 rows of every wave, parked for the epilogue from the second slot on
+  static constexpr int ParkBytes = Waves * 32 * 32 * NI * 4;
+  static_assert(Slot + ParkBytes <= SRing, "the parked rows fit beside the first slot");
   static_assert(DA % 2 == 0 && DB % 2 == 0, "a wave's loads of a slot come in pairs");
-  static_assert(Waves * (MI > 2 ? 2 : MI) * 32 * PadN * 4 <= Lds, "the epilogue's rows fit");
 };
 
 __device__ __forceinline__ v4i buffer_of(const void* base, int64_t bytes) {
@@ -59,6 +62,7 @@ template <int N>
 __device__ __forceinline__ void wait_loads() {
   asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(N) : "memory");
 }
+__device__ __forceinline__ void wait_lds() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
 __device__ __forceinline__ void barrier() {
   asm volatile("s_barrier" ::: "memory");
 }
@@ -162,12 +166,12 @@ __device__ __forceinline__ void multiply(f32x16 (&c)[MI][NI], const Frag<A8> (&a
   }
 }
 
-// Workgroup `b` of `total` as the b-th of a list in which every XCD (workgroups are dealt
-// to the eight in turn) walks consecutive entries, so that tiles which share operand
-// rows share an L2.
-__device__ __forceinline__ int xcd_order(int b, int total) {
-  const int x = b & 7, q = total >> 3, r = total & 7;
-  return x * q + (x < r ? x : r) + (b >> 3);
+// A workgroup takes entry `turn` of its share of the tiles. Workgroups are dealt to the eight
+// XCDs in turn; entries are ordered so that the workgroups of an XCD hold consecutive
+// ones, which share operand rows in its L2.
+__device__ __forceinline__ int64_t list_entry(int64_t turn) {
+  const int grid = gridDim.x, x = blockIdx.x & 7, q = grid >> 3, r = grid & 7;
+  return turn * grid + x * q + (x < r ? x : r) + (blockIdx.x >> 3);
 }
 
 template <bool A8, bool B8, bool EXACT, int MI, int NI, int WN, int R, bool ODDK, bool WG, typename T>
@@ -177,72 +181,77 @@ __global__ __launch_bounds__(128 * WN, MI *NI > 8 ? 1 : 2) void mm_tile_kernel(M
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r = lane & 31, h = lane >> 5;
 
-  // the tile
   const bool listed = p.offsets && !WG;  // its row tiles are known on the device only
-  const int a_rows = WG ? (int)p.n : 0, b_rows = WG ? (int)p.k : (int)p.n;
   const int row_tiles = listed ? segment_tiles(p.offsets, p.groups, p.rows, G::BM)
-                        : WG   ? (a_rows + G::BM - 1) / G::BM
-                               : (int)((p.rows + G::BM - 1) / G::BM);
+                               : (int)(((WG ? p.n : p.rows) + G::BM - 1) / G::BM);
   const int64_t total = (int64_t)row_tiles * col_tiles * (WG ? p.groups : 1);
-  if ((int64_t)blockIdx.x >= total) return;
-  // Weight gradient: the experts one after the other, each over all XCDs, for their tiles
-  // cost what they have tokens.
-  const int listed_tiles = WG ? row_tiles * col_tiles : (int)total;
-  const int group = WG ? blockIdx.x / listed_tiles : 0;
-  const int at = xcd_order(blockIdx.x - group * listed_tiles, listed_tiles);
-  constexpr int Group = 8;  // row tiles walked together over the columns
-  const int band = at / (Group * col_tiles), in_band = at - band * (Group * col_tiles);
-  const int tall = row_tiles - band * Group < Group ? row_tiles - band * Group : Group;
-  const int row_tile = band * Group + in_band % tall, col_tile = in_band / tall;
-  Segment s{0, 0, p.rows, row_tile};
-  if (listed && !find_segment(p.offsets, p.groups, p.rows, G::BM, row_tile, s)) return;
-  // Weight gradient: the contraction runs over the expert's tokens, whose first byte of a
-  // column lies `shift` past a 16-byte boundary.
-  int64_t depth = p.k;
-  int shift = 0, first_slot = 0;
-  if constexpr (WG) {
-    s.expert = group;
-    s.begin = clamp_row(p.offsets[group], p.rows);
-    depth = clamp_row(p.offsets[group + 1], p.rows) - s.begin;
-    depth = depth < 0 ? 0 : depth;
-    shift = (int)(s.begin & 15);
-    first_slot = segment_tiles(p.offsets, group, p.rows, 128);
-  }
-
   const int64_t abytes = WG ? p.ld_a : A8 ? p.k : p.k / 2, bbytes = WG ? p.ld_b : B8 ? p.k : p.k / 2;
   const int64_t asbytes = WG ? 4 * p.ld_as : A8 ? p.k / 128 * 4 : p.k / 32;
   const int64_t bsbytes = WG ? 4 * p.ld_bs : B8 ? p.k / 128 * 4 : p.k / 32;
-  // first rows and row counts of the operands' tiles; orow0 is the tile's first row of d
-  const int64_t arow0 = WG ? (int64_t)row_tile * G::BM : s.begin + (int64_t)s.tile * G::BM;
-  const int64_t brow0 = (WG ? 0 : (int64_t)s.expert * p.n) + (int64_t)col_tile * G::BN;
-  const int64_t orow0 = WG ? group * p.n + arow0 : arow0;
-  const int64_t aleft = WG ? a_rows - arow0 : s.count - (int64_t)s.tile * G::BM;
-  const int64_t bleft = b_rows - (int64_t)col_tile * G::BN;
-  const int arows = (int)(aleft < G::BM ? aleft : G::BM), brows = (int)(bleft < G::BN ? bleft : G::BN);
-  const int64_t from = WG ? s.begin - shift : 0;  // bytes of a row before the first piece
-  const v4i abuf = buffer_of(p.a + arow0 * abytes + from, arows * abytes - from);
-  const v4i bbuf = buffer_of(p.b + brow0 * bbytes + from, brows * bbytes - from);
-  const uint8_t* ascale = static_cast<const uint8_t*>(p.a_scales) + arow0 * asbytes;
-  const uint8_t* bscale = static_cast<const uint8_t*>(p.b_scales) + brow0 * bsbytes;
-  const v4i asbuf = buffer_of(ascale, arows * asbytes);
-  const v4i bsbuf = buffer_of(bscale, brows * bsbytes);
+  const uint32_t apitch = (uint32_t)(16 * abytes), bpitch = (uint32_t)(16 * bbytes);
+  const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)lds;
 
+  // The tile in work: its expert, first row of d and first column, rows and columns there are,
+  int expert = 0, arows = 0, brows = 0;
+  int64_t orow0 = 0, col0 = 0;
+  // its operands. Weight gradient: the contraction runs over the expert's tokens, whose first
+  // byte of a column lies `shift` past a 16-byte boundary; first_slot: their first scale.
+  int64_t depth = 0;
+  int shift = 0, first_slot = 0;
+  v4i abuf = {}, bbuf = {}, asbuf = {}, bsbuf = {};
+  const uint8_t *ascale = nullptr, *bscale = nullptr;
   // Byte offsets of this lane's pieces in a wave's first two loads of a slot; the others lie
   // whole rows further on. Rows past the tile's last are past the buffer's end: zeros.
   uint32_t va[2], vb[2];
+  int turns = 0, halves = 0;  // slots of an MXFP4 operand, of an FP8 operand
+  int tail = 0;               // blocks of the last turn, 0: all eight
+  int last_steps = 0;
+  auto set_up = [&](int64_t entry) {
+    if (entry >= total) return false;
+    expert = WG ? (int)(entry / ((int64_t)row_tiles * col_tiles)) : 0;
+    const int at = (int)(entry - (int64_t)expert * row_tiles * col_tiles);
+    constexpr int Group = 8;  // row tiles walked together over the columns
+    const int band = at / (Group * col_tiles), in_band = at - band * (Group * col_tiles);
+    const int tall = row_tiles - band * Group < Group ? row_tiles - band * Group : Group;
+    const int row_tile = band * Group + in_band % tall, col_tile = in_band / tall;
+    Segment s{expert, 0, p.rows, row_tile};
+    if (listed && !find_segment(p.offsets, p.groups, p.rows, G::BM, row_tile, s)) return false;
+    depth = p.k;
+    if constexpr (WG) {
+      s.begin = clamp_row(p.offsets[expert], p.rows);
+      depth = clamp_row(p.offsets[expert + 1], p.rows) - s.begin;
+      depth = depth < 0 ? 0 : depth;
+      shift = (int)(s.begin & 15);
+      first_slot = segment_tiles(p.offsets, expert, p.rows, 128);
+    }
+    expert = s.expert;
+    const int64_t arow0 = WG ? (int64_t)row_tile * G::BM : s.begin + (int64_t)s.tile * G::BM;
+    col0 = (int64_t)col_tile * G::BN;
+    const int64_t brow0 = (WG ? 0 : (int64_t)expert * p.n) + col0;
+    orow0 = WG ? expert * p.n + arow0 : arow0;
+    const int64_t aleft = WG ? p.n - arow0 : s.count - (int64_t)s.tile * G::BM;
+    const int64_t bleft = (WG ? p.k : p.n) - col0;
+    arows = (int)(aleft < G::BM ? aleft : G::BM);
+    brows = (int)(bleft < G::BN ? bleft : G::BN);
+    const int64_t from = WG ? s.begin - shift : 0;  // bytes of a row before the first piece
+    abuf = buffer_of(p.a + arow0 * abytes + from, arows * abytes - from);
+    bbuf = buffer_of(p.b + brow0 * bbytes + from, brows * bbytes - from);
+    ascale = static_cast<const uint8_t*>(p.a_scales) + arow0 * asbytes;
+    bscale = static_cast<const uint8_t*>(p.b_scales) + brow0 * bsbytes;
+    asbuf = buffer_of(ascale, arows * asbytes);
+    bsbuf = buffer_of(bscale, brows * bsbytes);
 #pragma unroll
-  for (int j = 0; j < 2; ++j) {
-    const int arow = (wave * G::DA + j) * 8 + lane / 8, brow = (wave * G::DB + j) * 8 + lane / 8;
-    va[j] = (uint32_t)(arow * abytes) + 16 * piece(arow, lane % 8);
-    vb[j] = (uint32_t)(brow * bbytes) + 16 * piece(brow, lane % 8);
-  }
-  const uint32_t apitch = (uint32_t)(16 * abytes), bpitch = (uint32_t)(16 * bbytes);
-  const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)lds;
-  const int turns = (int)((depth + 255) / 256);
-  const int halves = (int)(WG ? (depth + 127) / 128 : depth / 128);  // slots of an FP8 operand
-  // blocks of the last turn, 0: all eight
-  const int tail = WG ? 4 * (halves & 1) : (int)(depth % 256) / 32;
-  const int last_steps = tail ? (tail + 1) / 2 : 4;
+    for (int j = 0; j < 2; ++j) {
+      const int arow = (wave * G::DA + j) * 8 + lane / 8, brow = (wave * G::DB + j) * 8 + lane / 8;
+      va[j] = (uint32_t)(arow * abytes) + 16 * piece(arow, lane % 8);
+      vb[j] = (uint32_t)(brow * bbytes) + 16 * piece(brow, lane % 8);
+    }
+    turns = (int)((depth + 255) / 256);
+    halves = (int)(WG ? (depth + 127) / 128 : depth / 128);
+    tail = WG ? 4 * (halves & 1) : (int)(depth % 256) / 32;
+    last_steps = tail ? (tail + 1) / 2 : 4;
+    return true;
+  };
 
   // Before the last turn of an MXFP4 operand is loaded: pieces past the rows' end repeat the
   // row's first one.
@@ -267,13 +276,15 @@ __global__ __launch_bounds__(128 * WN, MI *NI > 8 ? 1 : 2) void mm_tile_kernel(M
     v4i buf = abuf;
     buf[2] = q < (A8 ? halves : turns) ? buf[2] : 0;
     const uint32_t at = (uint32_t)q * 128;
-    load_lds16(buf, va[j & 1] + (j >> 1) * apitch + (WG ? at : 0), WG ? 0 : at, lds0 + (q & (R - 1)) * G::ASlot + (wave * G::DA + j) * 1024);
+    load_lds16(buf, va[j & 1] + (j >> 1) * apitch + (WG ? at : 0), WG ? 0 : at,
+               lds0 + (q & (R - 1)) * G::Slot + (wave * G::DA + j) * 1024);
   };
   auto load_b = [&](int q, int j) {
     v4i buf = bbuf;
     buf[2] = q < (B8 ? halves : turns) ? buf[2] : 0;
     const uint32_t at = (uint32_t)q * 128;
-    load_lds16(buf, vb[j & 1] + (j >> 1) * bpitch + (WG ? at : 0), WG ? 0 : at, lds0 + G::BRing + (q & (R - 1)) * G::BSlot + (wave * G::DB + j) * 1024);
+    load_lds16(buf, vb[j & 1] + (j >> 1) * bpitch + (WG ? at : 0), WG ? 0 : at,
+               lds0 + G::ASlot + (q & (R - 1)) * G::Slot + (wave * G::DB + j) * 1024);
   };
   // Weight gradient. Tokens [0, 128) of a group lie at bytes [shift, 128 + shift) of nine
   // 16-byte pieces. The first piece's leading bytes, which belong to other tokens, are
@@ -313,7 +324,7 @@ __global__ __launch_bounds__(128 * WN, MI *NI > 8 ? 1 : 2) void mm_tile_kernel(M
       const int row = i / 9, c = i % 9, keep = last + shift - 16 * c;  // leading bytes that stay
       if (keep >= 16 || (c == 8 && shift == 0)) continue;
       const int x = row < G::BM ? row : row - G::BM;
-      uint8_t* slot = row < G::BM ? lds + (q & (R - 1)) * G::ASlot : lds + G::BRing + (q & (R - 1)) * G::BSlot;
+      uint8_t* slot = row < G::BM ? lds + (q & (R - 1)) * G::Slot : lds + G::ASlot + (q & (R - 1)) * G::Slot;
       v4i* at = c == 8 ? reinterpret_cast<v4i*>(lds + G::XRing + (q & (R - 1)) * G::XSlot + row * 16)
                        : reinterpret_cast<v4i*>(slot + x * 128 + 16 * piece(x, c));
       v4i w = *at;
@@ -413,8 +424,8 @@ __global__ __launch_bounds__(128 * WN, MI *NI > 8 ? 1 : 2) void mm_tile_kernel(M
   };
   // The last turn's last step has one block where `tail` is odd: clears the other one.
   auto clear_tail = [&]() {
-    uint8_t* a = lds + ((turns - 1) & (R - 1)) * G::ASlot;
-    uint8_t* b = lds + G::BRing + ((turns - 1) & (R - 1)) * G::BSlot;
+    uint8_t* a = lds + ((turns - 1) & (R - 1)) * G::Slot;
+    uint8_t* b = lds + G::ASlot + ((turns - 1) & (R - 1)) * G::Slot;
     for (int row = threadIdx.x; row < G::SRows; row += G::Threads) {
       const int x = row < G::BM ? row : row - G::BM;
       *reinterpret_cast<v4i*>((row < G::BM ? a : b) + x * 128 + 16 * piece(x, tail)) = v4i{0, 0, 0, 0};
@@ -432,7 +443,7 @@ __global__ __launch_bounds__(128 * WN, MI *NI > 8 ? 1 : 2) void mm_tile_kernel(M
   Frag<A8> fa[Roll ? 1 : 2][MI];
   Frag<B8> fb[2][NI];
   uint32_t sa[MI], sb[NI], ra[MI], rb[NI];
-  f32x16 c[MI][NI] = {};
+  f32x16 c[MI][NI];
   // The sums pass through an empty statement after every step: the products, which have
   // no side effects, would else sink below the barriers and keep every fragment alive.
   auto pin = [&]() {
@@ -447,13 +458,13 @@ __global__ __launch_bounds__(128 * WN, MI *NI > 8 ? 1 : 2) void mm_tile_kernel(M
       }
   };
   auto read_a = [&](int t, int s, int i) {
-    Frag<A8> f = read_frag<A8, EXACT>(lds + ((A8 ? 2 * t + (s >> 1) : t) & (R - 1)) * G::ASlot, abase, i, s);
+    Frag<A8> f = read_frag<A8, EXACT>(lds + ((A8 ? 2 * t + (s >> 1) : t) & (R - 1)) * G::Slot, abase, i, s);
     if (WG && (s & 1) == 0) f.w[0] = merge_ninth(f.w[0], 2 * t + (s >> 1), row16(abase) + 512 * i);
     return f;
   };
   // Fragments of step s of turn t: B's, and A's where they are not replaced one by one.
   auto read_step = [&](int t, int s) {
-    const uint8_t* b = lds + G::BRing + ((B8 ? 2 * t + (s >> 1) : t) & (R - 1)) * G::BSlot;
+    const uint8_t* b = lds + G::ASlot + ((B8 ? 2 * t + (s >> 1) : t) & (R - 1)) * G::Slot;
     if constexpr (!Roll) {
 #pragma unroll
       for (int i = 0; i < MI; ++i) fa[s & 1][i] = read_a(t, s, i);
@@ -481,76 +492,40 @@ __global__ __launch_bounds__(128 * WN, MI *NI > 8 ? 1 : 2) void mm_tile_kernel(M
     for (int j = 0; j < NI; ++j) sb[j] = scale_reg<B8>(rb[j], h);
   };
 
-  if (!WG || turns > 0) {
-  if constexpr (ODDK) {
-    fetch_scales(0);
-    park_scales(0);
-  } else {
-#pragma unroll
-    for (int c = 0; c < G::Ahead; ++c)
-      if (c == 0 || 2 * c < turns) load_scales(c);
-  }
-  // the slots, of the last ones only what the steps to come do not load
-#pragma unroll
-  for (int q = 0; q < R; ++q) {
-    trim(q);
-    load_ninth(q);
-#pragma unroll
-    for (int j = 0; j < (q < R - 1 ? G::DA : A8 ? G::DA / 2 : G::DA < 3 ? G::DA : 3); ++j) load_a(q, j);
-#pragma unroll
-    for (int j = 0; j < (q < R - 1 ? G::DB : B8 ? G::DB / 2 : 0); ++j) load_b(q, j);
-  }
-  constexpr int Now = (A8 ? G::DA / 2 : G::DA < 3 ? G::DA : 3) + (B8 ? G::DB / 2 : 0);
-  wait_loads<Now + (R - 2) * (G::DA + G::DB)>();
-  barrier();
-  if (ODDK && (tail & 1) && turns == 1) clear_tail();
-  if (WG && halves == 1) clear_group(0);
-  read_step(0, 0);
-  if constexpr (Roll) {
-#pragma unroll
-    for (int i = 0; i < MI; ++i) fa[0][i] = read_a(0, 0, i);
-  }
-  read_scales(0);
-  select_scales();
-
-  for (int t = 0; t + 1 < turns; ++t) {
-    // addresses and masks are formed where used, not held
-    asm volatile("" : "+v"(abase), "+v"(bbase));
-    if constexpr (WG) asm volatile("" : "+v"(keep_second));
+  // The loads that start a tile: its first scales and slot 0, then the other slots, of the
+  // last one only what the steps to come do not load.
+  auto start_first = [&]() {
+    if (WG && turns == 0) return;
     if constexpr (ODDK) {
-      // chunk c + 1 is fetched in the first turn of chunk c and parked in the second
-      if ((t & 1) == 0 && t + 2 < turns) fetch_scales((t >> 1) + 1);
-      if ((t & 1) == 1 && t + 1 < turns) park_scales((t >> 1) + 1);
-    }
+      fetch_scales(0);
+      park_scales(0);
+    } else {
 #pragma unroll
-    for (int s = 0; s < 4; ++s) {
-      // the next slots have landed, and every wave has its last fragments of the current ones
-      if (s == 3 || (s == 1 && (A8 || B8))) {
-        wait_loads<G::Younger>();
-        barrier();
-        if (WG && s == 3 && t + 2 == turns && (halves & 1)) clear_group(halves - 1);
-      }
-      if (s == 3) {
-        if (ODDK && (tail & 1) && t + 2 == turns) clear_tail();
-        trim(t + R);
-        if constexpr (!ODDK)
-          if ((t & 1) == 0 && t + 2 * G::Ahead < turns) load_scales((t >> 1) + G::Ahead);
-      }
-      const int tn = s == 3 ? t + 1 : t, sn = (s + 1) & 3;
-      read_step(tn, sn);
-      if (s & 1) read_scales(2 * t + (s + 1) / 2);
-      __builtin_amdgcn_sched_barrier(0);
-      multiply<A8, B8, EXACT, MI, NI>(c, fa[Roll ? 0 : s & 1], fb[s & 1], sa, sb, s & 1, [&](int u) {
-        if constexpr (Roll) fa[0][u] = read_a(tn, sn, u);
-        load_part(t, s, u);
-      });
-      pin();
-      __builtin_amdgcn_sched_barrier(0);
-      if (s & 1) select_scales();
+      for (int c = 0; c < G::Ahead; ++c)
+        if (c == 0 || 2 * c < turns) load_scales(c);
     }
-  }
+    trim(0);
+    load_ninth(0);
+#pragma unroll
+    for (int j = 0; j < G::DA; ++j) load_a(0, j);
+#pragma unroll
+    for (int j = 0; j < G::DB; ++j) load_b(0, j);
+  };
+  constexpr int PartA = A8 ? G::DA / 2 : G::DA < 3 ? G::DA : 3, PartB = B8 ? G::DB / 2 : 0;
+  auto start_rest = [&]() {
+    if (WG && turns == 0) return;
+#pragma unroll
+    for (int q = 1; q < R; ++q) {
+      trim(q);
+      load_ninth(q);
+#pragma unroll
+      for (int j = 0; j < (q < R - 1 ? G::DA : PartA); ++j) load_a(q, j);
+#pragma unroll
+      for (int j = 0; j < (q < R - 1 ? G::DB : PartB); ++j) load_b(q, j);
+    }
+  };
   // the last turn: one to four steps (two or four where k is a multiple of 128)
-  auto finish = [&](int s) {
+  auto last_step = [&](int s) {
     if (s + 1 < last_steps) {
       read_step(turns - 1, s + 1);
       if (s == 1) read_scales(2 * turns - 1);
@@ -564,48 +539,119 @@ __global__ __launch_bounds__(128 * WN, MI *NI > 8 ? 1 : 2) void mm_tile_kernel(M
     pin();
     if (s == 1) select_scales();
   };
-  finish(0);
-  if (!ODDK || last_steps > 1) {
-    if constexpr (A8 || B8) {
-      wait_loads<G::Younger>();
-      barrier();
-      if (WG && 2 * turns == halves) clear_group(halves - 1);
-    }
-    finish(1);
-    if (last_steps > 2) {
-      finish(2);
-      if (!ODDK || last_steps > 3) finish(3);
-    }
-  }
-  }
 
-  // Epilogue: a block of rows at a time through LDS, so that rows leave as whole runs.
-  wait_loads<0>();
-  barrier();
-  constexpr int V = sizeof(T) == 2 ? 8 : 4, PerRow = 32 * NI / V, RowsAtOnce = 64 / PerRow;
-  constexpr int Park = MI > 2 ? 2 : MI;  // 32-row blocks parked at a time
-  float* park = reinterpret_cast<float*>(lds) + wave * Park * 32 * G::PadN;
-  const int prow = lane / PerRow, pcol = (lane % PerRow) * V;
-  RunEpilogue<T, V> out(p.ep, s.expert, (int64_t)col_tile * G::BN + wn * 32 * NI + pcol);
-#pragma unroll 1
-  for (int block = 0; block < MI / Park; ++block) {
+  if (!set_up(list_entry(0))) return;
+  start_first();
+  for (int64_t entry = 0;; ++entry) {
+    start_rest();
 #pragma unroll
-    for (int i = 0; i < MI; ++i) {
-      if (i / Park == block) {
-        float* to = park + (i % Park * 32 + r) * G::PadN + 4 * h;
+    for (int i = 0; i < MI; ++i)
 #pragma unroll
-        for (int j = 0; j < NI; ++j)
+      for (int j = 0; j < NI; ++j) c[i][j] = f32x16{};
+    if (!WG || turns > 0) {
+      wait_loads<PartA + PartB + (R - 2) * (G::DA + G::DB)>();
+      barrier();
+      if (ODDK && (tail & 1) && turns == 1) clear_tail();
+      if (WG && halves == 1) clear_group(0);
+      read_step(0, 0);
+      if constexpr (Roll) {
 #pragma unroll
-          for (int q = 0; q < 4; ++q)
-            *reinterpret_cast<float4*>(to + 32 * j + 8 * q) =
-                make_float4(c[i][j][4 * q], c[i][j][4 * q + 1], c[i][j][4 * q + 2], c[i][j][4 * q + 3]);
+        for (int i = 0; i < MI; ++i) fa[0][i] = read_a(0, 0, i);
+      }
+      read_scales(0);
+      select_scales();
+
+      for (int t = 0; t + 1 < turns; ++t) {
+        // addresses and masks are formed where used, not held
+        asm volatile("" : "+v"(abase), "+v"(bbase));
+        if constexpr (WG) asm volatile("" : "+v"(keep_second));
+        if constexpr (ODDK) {
+          // chunk c + 1 is fetched in the first turn of chunk c and parked in the second
+          if ((t & 1) == 0 && t + 2 < turns) fetch_scales((t >> 1) + 1);
+          if ((t & 1) == 1 && t + 1 < turns) park_scales((t >> 1) + 1);
+        }
+#pragma unroll
+        for (int s = 0; s < 4; ++s) {
+          // the next slots have landed, and every wave has its last fragments of the current ones
+          if (s == 3 || (s == 1 && (A8 || B8))) {
+            wait_loads<G::Younger>();
+            barrier();
+            if (WG && s == 3 && t + 2 == turns && (halves & 1)) clear_group(halves - 1);
+          }
+          if (s == 3) {
+            if (ODDK && (tail & 1) && t + 2 == turns) clear_tail();
+            trim(t + R);
+            if constexpr (!ODDK)
+              if ((t & 1) == 0 && t + 2 * G::Ahead < turns) load_scales((t >> 1) + G::Ahead);
+          }
+          const int tn = s == 3 ? t + 1 : t, sn = (s + 1) & 3;
+          read_step(tn, sn);
+          if (s & 1) read_scales(2 * t + (s + 1) / 2);
+          __builtin_amdgcn_sched_barrier(0);
+          multiply<A8, B8, EXACT, MI, NI>(c, fa[Roll ? 0 : s & 1], fb[s & 1], sa, sb, s & 1, [&](int u) {
+            if constexpr (Roll) fa[0][u] = read_a(tn, sn, u);
+            load_part(t, s, u);
+          });
+          pin();
+          __builtin_amdgcn_sched_barrier(0);
+          if (s & 1) select_scales();
+        }
+      }
+      last_step(0);
+      if (!ODDK || last_steps > 1) {
+        if constexpr (A8 || B8) {
+          wait_loads<G::Younger>();
+          barrier();
+          if (WG && 2 * turns == halves) clear_group(halves - 1);
+        }
+        last_step(1);
+        if (last_steps > 2) {
+          last_step(2);
+          if (!ODDK || last_steps > 3) last_step(3);
+        }
       }
     }
-    __builtin_amdgcn_wave_barrier();
-    const int first = wm * 32 * MI + block * Park * 32 + prow;
-    out.rows(p.ep, park + prow * G::PadN + pcol, RowsAtOnce * G::PadN, orow0 + first, arows - first, RowsAtOnce,
-             Park * 32 / RowsAtOnce);
-    __builtin_amdgcn_wave_barrier();
+    // Every wave is done with the slots: the next tile's first loads start before this one's
+    // results are finished and stored.
+    wait_loads<0>();
+    barrier();
+    const int64_t out_row = orow0 + wm * 32 * MI, out_col = col0 + wn * 32 * NI;
+    const int out_rows = arows - wm * 32 * MI, out_expert = expert;
+    const bool more = set_up(list_entry(entry + 1));
+    if (more) start_first();
+
+    // Epilogue: 32 rows at a time through LDS, so that rows leave as whole runs.
+    constexpr int V = sizeof(T) == 2 ? 8 : 4, PerRow = 32 * NI / V, RowsAtOnce = 64 / PerRow;
+    constexpr int Pieces = 8 * NI;  // 16-byte pieces of a parked row, exchanged so that no read or write collides
+    float* park = reinterpret_cast<float*>(lds + G::Slot) + wave * 32 * 32 * NI;
+    const int prow = lane / PerRow, pcol = lane % PerRow * V;
+    RunEpilogue<T, V> out(p.ep, out_expert, out_col + pcol);
+#pragma unroll
+    for (int i = 0; i < MI; ++i) {
+#pragma unroll
+      for (int j = 0; j < NI; ++j)
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          *reinterpret_cast<float4*>(park + r * 32 * NI + 4 * ((8 * j + 2 * q + h) ^ (r & (Pieces - 1)))) =
+              make_float4(c[i][j][4 * q], c[i][j][4 * q + 1], c[i][j][4 * q + 2], c[i][j][4 * q + 3]);
+      __builtin_amdgcn_wave_barrier();
+      out.template rows<32 / RowsAtOnce, RowsAtOnce>(
+          p.ep,
+          [&](int k, float(&z)[V]) {
+            const int row = prow + k * RowsAtOnce;
+#pragma unroll
+            for (int v = 0; v < V; v += 4) {
+              const float4 x = *reinterpret_cast<const float4*>(
+                  park + row * 32 * NI + 4 * ((pcol / 4 + v / 4) ^ (row & (Pieces - 1))));
+              z[v] = x.x, z[v + 1] = x.y, z[v + 2] = x.z, z[v + 3] = x.w;
+            }
+          },
+          out_row + 32 * i + prow, out_rows - 32 * i - prow);
+      __builtin_amdgcn_wave_barrier();
+    }
+    if (!more) return;
+    wait_lds();
+    barrier();
   }
 }
 
@@ -620,7 +666,8 @@ hipError_t launch_tile(const MmLaunch& a, hipStream_t st) {
   static const hipError_t set =
       hipFuncSetAttribute(reinterpret_cast<const void*>(k), hipFuncAttributeMaxDynamicSharedMemorySize, G::Lds);
   if (set != hipSuccess) return set;
-  k<<<dim3((uint32_t)(row_tiles * col_tiles)), G::Threads, G::Lds, st>>>(a, (int)col_tiles);
+  const int64_t tiles = row_tiles * col_tiles;
+  k<<<dim3((uint32_t)(tiles < kCUs ? tiles : kCUs)), G::Threads, G::Lds, st>>>(a, (int)col_tiles);
   return hipGetLastError();
 }
 
