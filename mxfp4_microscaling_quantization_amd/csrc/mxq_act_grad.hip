@@ -50,35 +50,49 @@ __global__ __launch_bounds__(256) void act_grad_kernel(ActGradLaunch p, int col_
   const bool vec = p.n % 8 == 0, gated = p.act == kActSwiglu;
   float sum[8] = {};
   if (left > 0) {
-    for (int r = wave; r < count; r += 4) {
-      const int64_t row = s.begin + first + r, at = row * p.n + col;
-      float z[8], dz[8];
-      load_run<T>(static_cast<const T*>(p.z) + at, z, left, vec);
-      if (gated) {
-        const T* dy = static_cast<const T*>(p.dy) + row * (p.n / 2) + col / 2;
-        float g[4];
-        if (vec) {
-          get_run<T, 4>(dy, g);
+    // four rows of a wave in flight: their loads go ahead of the first one's arithmetic
+    for (int r0 = wave; r0 < count; r0 += 16) {
+      float z[4][8], dy[4][8];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int64_t row = s.begin + first + (r0 + 4 * u < count ? r0 + 4 * u : count - 1);
+        load_run<T>(static_cast<const T*>(p.z) + row * p.n + col, z[u], left, vec);
+        if (gated) {
+          const T* q = static_cast<const T*>(p.dy) + row * (p.n / 2) + col / 2;
+          float g[4];
+          if (vec) {
+            get_run<T, 4>(q, g);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) g[i] = 2 * i < left ? Out<T>::get(q + i) : 0.0f;
+          }
+#pragma unroll
+          for (int i = 0; i < 4; ++i) dy[u][2 * i] = g[i];
+        } else {
+          load_run<T>(static_cast<const T*>(p.dy) + row * p.n + col, dy[u], left, vec);
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        if (r0 + 4 * u >= count) break;
+        float dz[8];
+        if (gated) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float g = z[u][2 * i], sg = sigmoid_f(g), d = dy[u][2 * i];
+            dz[2 * i] = d * z[u][2 * i + 1] * (sg * fmaf(g, 1.0f - sg, 1.0f));
+            dz[2 * i + 1] = d * (g * sg);
+          }
         } else {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) g[i] = 2 * i < left ? Out<T>::get(dy + i) : 0.0f;
+          for (int i = 0; i < 8; ++i) dz[i] = act_grad_f(dy[u][i], z[u][i], p.act);
         }
+        if (SUM) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          dz[2 * i] = act_grad_f(g[i], z[2 * i], kActSilu) * z[2 * i + 1];
-          dz[2 * i + 1] = g[i] * (z[2 * i] * sigmoid_f(z[2 * i]));
+          for (int i = 0; i < 8; ++i) sum[i] += dz[i];
         }
-      } else {
-        float dy[8];
-        load_run<T>(static_cast<const T*>(p.dy) + at, dy, left, vec);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) dz[i] = act_grad_f(dy[i], z[i], p.act);
+        store_run<T, 8>(static_cast<T*>(p.dz) + (s.begin + first + r0 + 4 * u) * p.n + col, nullptr, dz, left, vec);
       }
-      if (SUM) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) sum[i] += dz[i];
-      }
-      store_run<T, 8>(static_cast<T*>(p.dz) + at, nullptr, dz, left, vec);
     }
   }
   if constexpr (SUM) {
@@ -92,10 +106,15 @@ __global__ __launch_bounds__(256) void act_grad_kernel(ActGradLaunch p, int col_
   }
 }
 
-// db[g] = the partial sums of the group's row blocks, in order.
-__global__ __launch_bounds__(256) void act_grad_sum_kernel(ActGradLaunch p, int col_tiles) {
-  const int g = blockIdx.x / col_tiles;
-  const int64_t col = (int64_t)(blockIdx.x % col_tiles) * 256 + threadIdx.x;
+// db[g] = the partial sums of the group's row blocks. A column has kLanes threads, each with
+// every kLanes-th block in order; their sums are added in order. (A group with a third of
+// the rows has hundreds of blocks: one thread after them all was the longest part.)
+constexpr int kLanes = 16;
+
+__global__ __launch_bounds__(64 * kLanes) void act_grad_sum_kernel(ActGradLaunch p, int col_tiles) {
+  __shared__ float sums[kLanes][64];
+  const int g = blockIdx.x / col_tiles, lane = threadIdx.x & 63, part = threadIdx.x >> 6;
+  const int64_t col = (int64_t)(blockIdx.x % col_tiles) * 64 + lane;
   int first = 0, blocks = (int)((p.rows + kActGradRows - 1) / kActGradRows);
   if (p.offsets) {
     first = segment_tiles(p.offsets, g, p.rows, kActGradRows);
@@ -105,10 +124,18 @@ __global__ __launch_bounds__(256) void act_grad_sum_kernel(ActGradLaunch p, int 
     const int most = (int)act_grad_blocks(p.rows, p.groups);
     blocks = first >= most ? 0 : first + blocks > most ? most - first : blocks;
   }
-  if (col >= p.n) return;
   float sum = 0.0f;
-  for (int b = 0; b < blocks; ++b) sum += p.partials[(int64_t)(first + b) * p.n + col];
-  p.db[(int64_t)g * p.n + col] = sum;
+  if (col < p.n) {
+    const float* q = p.partials + (int64_t)first * p.n + col;
+#pragma unroll 4
+    for (int b = part; b < blocks; b += kLanes) sum += q[(int64_t)b * p.n];
+  }
+  sums[part][lane] = sum;
+  __syncthreads();
+  if (part == 0 && col < p.n) {
+    for (int i = 1; i < kLanes; ++i) sum += sums[i][lane];
+    p.db[(int64_t)g * p.n + col] = sum;
+  }
 }
 
 template <typename T>
@@ -122,8 +149,8 @@ hipError_t launch_t(const ActGradLaunch& a, hipStream_t st) {
       act_grad_kernel<T, false><<<grid, 256, 0, st>>>(a, (int)col_tiles);
   }
   if (a.db) {
-    const int64_t sum_tiles = (a.n + 255) / 256;
-    act_grad_sum_kernel<<<dim3((uint32_t)(a.groups * sum_tiles)), 256, 0, st>>>(a, (int)sum_tiles);
+    const int64_t sum_tiles = (a.n + 63) / 64;
+    act_grad_sum_kernel<<<dim3((uint32_t)(a.groups * sum_tiles)), 64 * kLanes, 0, st>>>(a, (int)sum_tiles);
   }
   return hipGetLastError();
 }

@@ -136,7 +136,7 @@ mxq_status mxq_act_grad(const void* dy, const void* z, mxq_dtype dt, int64_t row
   if (n == 0 || n > kMaxDim || rows > kMaxDim || rows > ((int64_t)1 << 40) / n) return MXQ_ESHAPE;
   if (act == MXQ_ACT_SWIGLU && n % 2) return MXQ_ESHAPE;
   // the grids enumerate row blocks x column tiles and groups x column tiles
-  if (act_grad_blocks(rows, n_experts) * ((n + 511) / 512) >= kMaxGrid || n_experts * ((n + 255) / 256) >= kMaxGrid)
+  if (act_grad_blocks(rows, n_experts) * ((n + 511) / 512) >= kMaxGrid / 64 || n_experts * ((n + 63) / 64) >= kMaxGrid / 256)
     return MXQ_ESHAPE;
   if (!aligned(dy, 16) || !aligned(z, 16) || !aligned(dz, 16) || !aligned(db, 16) || !aligned(workspace, 16) ||
       !aligned(offsets, 8))

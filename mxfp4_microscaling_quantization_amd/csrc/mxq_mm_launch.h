@@ -35,6 +35,11 @@ struct MmLaunch {
 hipError_t launch_gemm_rows(const MmLaunch& a, bool few, hipStream_t st);
 // The tiled kernel: 256 x 256 results of a workgroup (large) or 128 x 128.
 hipError_t launch_gemm_tiles(const MmLaunch& a, bool large, hipStream_t st);
+// Whether `each` results of rows x cols (extra_rows: started row tiles beyond those) take the
+// large tiles. One takes about 2.2 times a small one's time for four times its results, and 256
+// run at once (MXFP4, k 4096, large and small, us: 1024 x 4096 results 32.0 and 17.9,
+// 2048 x 4096 33.3 and 31.5, 4096 x 4096 40.0 and 58.2).
+bool large_tiles(int64_t rows, int64_t cols, int64_t extra_rows, int64_t each);
 hipError_t launch_gemm(const MmLaunch& a, hipStream_t st);
 
 // The weight gradient of every expert: a = dY's FP8 columns [n, ld_a], b = X's [k, ld_b],

@@ -695,9 +695,16 @@ hipError_t launch_gemm_tiles(const MmLaunch& a, bool large, hipStream_t st) {
   return large ? launch_sized<4, 2, 4, 4, 2, 2>(a, st) : launch_sized<2, 1, 4, 1, 4, 4>(a, st);
 }
 
+bool large_tiles(int64_t rows, int64_t cols, int64_t extra_rows, int64_t each) {
+  auto rounds = [&](int64_t side) {
+    const int64_t tiles = (rows / side + extra_rows + 1) * ((cols + side - 1) / side) * each;
+    return (tiles + kCUs - 1) / kCUs;
+  };
+  return 22 * rounds(256) <= 10 * rounds(128);
+}
+
 hipError_t launch_grouped_wgrad(const MmLaunch& a, hipStream_t st) {
-  const bool large = a.n > 128 && a.k > 128;
-  if (large)
+  if (large_tiles(a.n - 1, a.k, 0, a.groups))
     return a.ep.out_f32 ? launch_tile<true, true, true, 4, 4, 2, 2, false, true, float>(a, st)
                         : launch_tile<true, true, false, 4, 2, 4, 2, false, true, __bf16>(a, st);
   return a.ep.out_f32 ? launch_tile<true, true, true, 2, 1, 4, 4, false, true, float>(a, st)

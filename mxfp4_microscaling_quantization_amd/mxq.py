@@ -96,7 +96,8 @@ def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
 
 
 def _stream() -> int:
-    return torch.cuda.current_stream().cuda_stream
+    # the current device's current stream, without building a Stream object for it
+    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
 
 
 def _dtype_code(t: torch.Tensor) -> int:
@@ -263,30 +264,43 @@ def mxq_rht_amax(x: torch.Tensor, sign_mask: int, axis: str = "row",
 # uint8 codes [R, K/2] with uint8 E8M0 bytes [R, K/32], FP8 is E4M3 bytes [R, K] with
 # fp32 scales [R, K/128]; for experts' weights [E, N, ...].
 
+# scale dtype -> (format, elements of a code byte, elements of a scale)
+_OPERANDS = {torch.uint8: (OPERAND_MXFP4, 2, 32), torch.float32: (OPERAND_FP8, 1, 128)}
+_DTYPES = {torch.bfloat16: BF16, torch.float32: F32}
+
+
 def _operand(op, dims: int):
-    """(codes, scales, format, k) of an operand of `dims` dimensions, checked."""
+    """(code pointer, scale pointer, format, k, shape of the codes) of an operand of `dims`
+    dimensions, checked."""
     codes, scales = op
-    if scales.dtype == torch.uint8:
-        fmt, k, want = OPERAND_MXFP4, codes.shape[-1] * 2, codes.shape[-1] // 16
-    elif scales.dtype == torch.float32:
-        fmt, k, want = OPERAND_FP8, codes.shape[-1], codes.shape[-1] // 128
-    else:
+    kind = _OPERANDS.get(scales.dtype)
+    if kind is None:
         raise TypeError(f"unsupported scale dtype {scales.dtype}")
     if codes.dtype != torch.uint8:
         raise TypeError(f"unsupported code dtype {codes.dtype}")
-    if codes.dim() != dims or scales.dim() != dims or scales.shape[:-1] != codes.shape[:-1] or scales.shape[-1] != want:
-        raise ValueError(f"operand of {dims} dimensions expected, got codes {tuple(codes.shape)} and scales "
-                         f"{tuple(scales.shape)}")
+    fmt, per_code, per_scale = kind
+    shape, sshape = codes.shape, scales.shape
+    k = shape[-1] * per_code
+    if len(shape) != dims or sshape[:-1] != shape[:-1] or sshape[-1] != k // per_scale:
+        raise ValueError(f"operand of {dims} dimensions expected, got codes {tuple(shape)} and scales "
+                         f"{tuple(sshape)}")
     if not (codes.is_contiguous() and scales.is_contiguous()):
         raise ValueError("operands must be dense")
-    return codes, scales, fmt, k
+    return codes.data_ptr(), scales.data_ptr(), fmt, k, shape
 
 
-def _dense(t: Optional[torch.Tensor], shape, dtype, what: str) -> None:
-    if t is None:
-        return
+def _dense(t: torch.Tensor, shape, dtype, what: str) -> int:
+    """Pointer of a dense tensor of this shape and type, checked."""
     if t.shape != shape or t.dtype != dtype or not t.is_contiguous():
         raise ValueError(f"{what}: dense {dtype} {tuple(shape)} expected, got {t.dtype} {tuple(t.shape)}")
+    return t.data_ptr()
+
+
+def _float_code(dtype) -> int:
+    code = _DTYPES.get(dtype)
+    if code is None:
+        raise TypeError(f"unsupported dtype {dtype}")
+    return code
 
 
 def _offsets(offsets: torch.Tensor) -> int:
@@ -296,33 +310,39 @@ def _offsets(offsets: torch.Tensor) -> int:
 
 
 def _product(a, b, offsets, bias, act, residual, preact, out_dtype, out):
-    ac, asc, afmt, k = _operand(a, 2)
-    bc, bsc, bfmt, bk = _operand(b, 2 if offsets is None else 3)
+    ap, asp, afmt, k, ashape = _operand(a, 2)
+    bp, bsp, bfmt, bk, bshape = _operand(b, 2 if offsets is None else 3)
     if bk != k:
         raise ValueError(f"contracted dimensions differ: {k} and {bk}")
-    m, n, dev, code = ac.shape[0], bc.shape[-2], ac.device, _ACT[act]
-    dn = n // 2 if code == SWIGLU else n
-    d, z = out if out is not None else (None, None)
+    m, n, code = ashape[0], bshape[-2], _ACT[act]
+    shape = (m, n // 2 if code == SWIGLU else n)
+    d = z = None
+    if out is not None:
+        d, z = out
+        out_dtype = d.dtype
+    dt = _float_code(out_dtype)
     if d is None:
-        d = torch.empty((m, dn), dtype=out_dtype, device=dev)
+        d = a[0].new_empty(shape, dtype=out_dtype)
     else:
-        _dense(d, (m, dn), d.dtype, "out")
+        _dense(d, shape, out_dtype, "out")
     if preact and z is None:
-        z = torch.empty((m, n), dtype=d.dtype, device=dev)
-    _dense(z, (m, n), d.dtype, "z")
-    _dense(residual, (m, dn), d.dtype, "residual")
+        z = a[0].new_empty((m, n), dtype=out_dtype)
+    zp = None if z is None else _dense(z, (m, n), out_dtype, "z")
+    rp = None if residual is None else _dense(residual, shape, out_dtype, "residual")
+    bias_p, bdt = None, F32
     if bias is not None:
-        _dense(bias, bc.shape[:-1], bias.dtype, "bias")
-    dt, bdt = _dtype_code(d), F32 if bias is None else _dtype_code(bias)
+        bdt = _float_code(bias.dtype)
+        bias_p = _dense(bias, bshape[:-1], bias.dtype, "bias")
     if offsets is None:
-        _check(lib().mxq_gemm(_ptr(ac), _ptr(asc), afmt, _ptr(bc), _ptr(bsc), bfmt, m, n, k, _ptr(bias), bdt, code,
-                              _ptr(residual), _ptr(d), dt, _ptr(z), _stream()))
+        status = lib().mxq_gemm(ap, asp, afmt, bp, bsp, bfmt, m, n, k, bias_p, bdt, code, rp, d.data_ptr(), dt, zp,
+                                _stream())
     else:
         experts = _offsets(offsets)
-        if bc.shape[0] != experts:
-            raise ValueError(f"{bc.shape[0]} weights for {experts} experts")
-        _check(lib().mxq_grouped_gemm(_ptr(ac), _ptr(asc), afmt, _ptr(bc), _ptr(bsc), bfmt, m, n, k, _ptr(offsets),
-                                      experts, _ptr(bias), bdt, code, _ptr(residual), _ptr(d), dt, _ptr(z), _stream()))
+        if bshape[0] != experts:
+            raise ValueError(f"{bshape[0]} weights for {experts} experts")
+        status = lib().mxq_grouped_gemm(ap, asp, afmt, bp, bsp, bfmt, m, n, k, offsets.data_ptr(), experts, bias_p,
+                                        bdt, code, rp, d.data_ptr(), dt, zp, _stream())
+    _check(status)
     return (d, z) if preact else d
 
 
@@ -360,12 +380,16 @@ def mxq_grouped_wgrad(y, x, offsets: torch.Tensor, rows: int, add: Optional[torc
             raise ValueError("columns must have unit token stride")
     (yq, ys), (xq, xs) = y, x
     n, k = yq.shape[0], xq.shape[0]
-    d = out if out is not None else torch.empty((experts, n, k), dtype=out_dtype, device=yq.device)
-    _dense(d, (experts, n, k), d.dtype, "out")
-    _dense(add, (experts, n, k), d.dtype, "add")
-    _check(lib().mxq_grouped_wgrad(_ptr(yq), _ptr(ys), yq.stride(0), ys.stride(0), _ptr(xq), _ptr(xs), xq.stride(0),
-                                   xs.stride(0), rows, n, k, _ptr(offsets), experts, _ptr(add), _ptr(d),
-                                   _dtype_code(d), _stream()))
+    shape = (experts, n, k)
+    if out is None:
+        d = yq.new_empty(shape, dtype=out_dtype)
+    else:
+        d, out_dtype = out, out.dtype
+    dt, dp = _float_code(out_dtype), _dense(d, shape, out_dtype, "out")
+    addp = None if add is None else _dense(add, shape, out_dtype, "add")
+    _check(lib().mxq_grouped_wgrad(yq.data_ptr(), ys.data_ptr(), yq.stride(0), ys.stride(0), xq.data_ptr(),
+                                   xs.data_ptr(), xq.stride(0), xs.stride(0), rows, n, k, offsets.data_ptr(), experts,
+                                   addp, dp, dt, _stream()))
     return d
 
 
@@ -375,25 +399,25 @@ def mxq_act_grad(dy: torch.Tensor, z: torch.Tensor, act: str = "none", offsets: 
     """mxq_act_grad: dz = act'(z) dy for the z that a product kept, and with `bias_grad`
     also the bias gradient: (dz, db), db fp32 [N], or [E, N] with expert offsets. `out`
     may be z; `workspace` (uint8, mxq_act_grad_workspace bytes) is allocated if absent."""
-    rows, n = z.shape
-    code = _ACT[act]
-    _dense(z, (rows, n), z.dtype, "z")
-    _dense(dy, (rows, n // 2 if code == SWIGLU else n), z.dtype, "dy")
-    groups = 1 if offsets is None else _offsets(offsets)
-    dz = out if out is not None else torch.empty_like(z)
-    _dense(dz, z.shape, z.dtype, "out")
+    rows, n = shape = z.shape
+    code, dtype = _ACT[act], z.dtype
+    dt = _float_code(dtype)
+    zp = _dense(z, shape, dtype, "z")
+    dyp = _dense(dy, (rows, n // 2 if code == SWIGLU else n), dtype, "dy")
+    groups, offp = (1, None) if offsets is None else (_offsets(offsets), offsets.data_ptr())
+    dz = torch.empty_like(z) if out is None else out
+    dzp = _dense(dz, shape, dtype, "out")
+    dbp = wsp = None
     if bias_grad:
-        shape = (n,) if offsets is None else (groups, n)
+        db_shape = (n,) if offsets is None else (groups, n)
         if db is None:
-            db = torch.empty(shape, dtype=torch.float32, device=z.device)
-        _dense(db, shape, torch.float32, "db")
+            db = z.new_empty(db_shape, dtype=torch.float32)
+        dbp = _dense(db, db_shape, torch.float32, "db")
         need = lib().mxq_act_grad_workspace(rows, n, groups)
         if workspace is None:
-            workspace = torch.empty((need,), dtype=torch.uint8, device=z.device)
+            workspace = z.new_empty((need,), dtype=torch.uint8)
         elif workspace.numel() * workspace.element_size() < need:
             raise ValueError(f"workspace of {need} bytes expected")
-    else:
-        db = None
-    _check(lib().mxq_act_grad(_ptr(dy), _ptr(z), _dtype_code(z), rows, n, code, _ptr(offsets), groups, _ptr(dz),
-                              _ptr(db), _ptr(workspace), _stream()))
+        wsp = workspace.data_ptr()
+    _check(lib().mxq_act_grad(dyp, zp, dt, rows, n, code, offp, groups, dzp, dbp, wsp, _stream()))
     return (dz, db) if bias_grad else dz
