@@ -25,73 +25,97 @@ __device__ __forceinline__ float act_grad_f(float dy, float z, int act) {
   return dy;
 }
 
-template <typename T>
-__device__ __forceinline__ void load_run(const T* p, float (&v)[8], int64_t left, bool vec) {
-  if (vec) {
-    get_run<T, 8>(p, v);
-  } else {
+// V elements of a row, as they lie in memory: whole (VEC: every row starts on V elements; data
+// read once, so non-temporal) or one by one, those past the row's end as zeros.
+template <typename T, int V, bool VEC>
+struct Run {
+  T v[V];
+  __device__ __forceinline__ void load(const T* p, int64_t left) {
+    if constexpr (VEC) {
+      if constexpr (sizeof(v) == 8) {
+        const uint2 x = load_nt(reinterpret_cast<const uint2*>(p));
+        __builtin_memcpy(v, &x, 8);
+      } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = i < left ? Out<T>::get(p + i) : 0.0f;
+        for (int i = 0; i < (int)sizeof(v) / 16; ++i) {
+          const uint4 x = load_nt(reinterpret_cast<const uint4*>(p) + i);
+          __builtin_memcpy(v + i * 16 / sizeof(T), &x, 16);
+        }
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < V; ++i) v[i] = i < left ? p[i] : (T)0.0f;
+    }
   }
-}
+  __device__ __forceinline__ void store(T* p, int64_t left) const {
+    if constexpr (VEC) {
+#pragma unroll
+      for (int i = 0; i < (int)sizeof(v) / 16; ++i) {
+        uint4 x;
+        __builtin_memcpy(&x, v + i * 16 / sizeof(T), 16);
+        store_nt(reinterpret_cast<uint4*>(p) + i, x);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < V; ++i)
+        if (i < left) p[i] = v[i];
+    }
+  }
+};
 
-// One workgroup: up to 64 rows of one group, 512 columns. Its waves take every fourth
-// row; the sums of the four waves are added in order through LDS.
-template <typename T, bool SUM>
+// One workgroup: up to p.block_rows rows of one group, 512 columns. Its waves take every
+// fourth row, four of them in flight: their loads go ahead of the first one's arithmetic.
+// The sums of the four waves are added in order through LDS.
+// Bound by memory: 65536 x 4096 bf16 swiglu moves 1.34 GB.
+template <typename T, bool SUM, bool GATED, bool VEC>
 __global__ __launch_bounds__(256) void act_grad_kernel(ActGradLaunch p, int col_tiles) {
   __shared__ float sums[4][kCols];
+  constexpr int U = 4;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int block = blockIdx.x / col_tiles, col_tile = blockIdx.x % col_tiles;
   Segment s{0, 0, p.rows, block};
-  if (p.offsets && !find_segment(p.offsets, p.groups, p.rows, kActGradRows, block, s)) return;
-  const int64_t first = (int64_t)s.tile * kActGradRows;
-  const int count = (int)(s.count - first < kActGradRows ? s.count - first : kActGradRows);
+  if (p.offsets && !find_segment(p.offsets, p.groups, p.rows, p.block_rows, block, s)) return;
+  const int64_t first = (int64_t)s.tile * p.block_rows;
+  const int count = (int)(s.count - first < p.block_rows ? s.count - first : p.block_rows);
   const int64_t col = (int64_t)col_tile * kCols + lane * 8, left = p.n - col;
-  const bool vec = p.n % 8 == 0, gated = p.act == kActSwiglu;
   float sum[8] = {};
   if (left > 0) {
-    // four rows of a wave in flight: their loads go ahead of the first one's arithmetic
-    for (int r0 = wave; r0 < count; r0 += 16) {
-      float z[4][8], dy[4][8];
+    const int64_t dn = GATED ? p.n / 2 : p.n;
+    const T* z = static_cast<const T*>(p.z) + (s.begin + first) * p.n + col;
+    const T* dy = static_cast<const T*>(p.dy) + (s.begin + first) * dn + (GATED ? col / 2 : col);
+    T* dz = static_cast<T*>(p.dz) + (s.begin + first) * p.n + col;
+    for (int r0 = wave; r0 < count; r0 += 4 * U) {
+      Run<T, 8, VEC> zr[U];
+      Run<T, GATED ? 4 : 8, VEC> dr[U];
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        const int64_t row = s.begin + first + (r0 + 4 * u < count ? r0 + 4 * u : count - 1);
-        load_run<T>(static_cast<const T*>(p.z) + row * p.n + col, z[u], left, vec);
-        if (gated) {
-          const T* q = static_cast<const T*>(p.dy) + row * (p.n / 2) + col / 2;
-          float g[4];
-          if (vec) {
-            get_run<T, 4>(q, g);
-          } else {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) g[i] = 2 * i < left ? Out<T>::get(q + i) : 0.0f;
-          }
-#pragma unroll
-          for (int i = 0; i < 4; ++i) dy[u][2 * i] = g[i];
-        } else {
-          load_run<T>(static_cast<const T*>(p.dy) + row * p.n + col, dy[u], left, vec);
-        }
+      for (int u = 0; u < U; ++u) {
+        const int64_t row = r0 + 4 * u < count ? r0 + 4 * u : count - 1;
+        zr[u].load(z + row * p.n, left);
+        dr[u].load(dy + row * dn, GATED ? left / 2 : left);
       }
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
+      for (int u = 0; u < U; ++u) {
         if (r0 + 4 * u >= count) break;
-        float dz[8];
-        if (gated) {
+        float v[8];
+        if constexpr (GATED) {
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const float g = z[u][2 * i], sg = sigmoid_f(g), d = dy[u][2 * i];
-            dz[2 * i] = d * z[u][2 * i + 1] * (sg * fmaf(g, 1.0f - sg, 1.0f));
-            dz[2 * i + 1] = d * (g * sg);
+            const float g = (float)zr[u].v[2 * i], up = (float)zr[u].v[2 * i + 1], d = (float)dr[u].v[i];
+            const float sg = sigmoid_f(g);
+            v[2 * i] = d * up * (sg * fmaf(g, 1.0f - sg, 1.0f));
+            v[2 * i + 1] = d * (g * sg);
           }
         } else {
 #pragma unroll
-          for (int i = 0; i < 8; ++i) dz[i] = act_grad_f(dy[u][i], z[u][i], p.act);
+          for (int i = 0; i < 8; ++i) v[i] = act_grad_f((float)dr[u].v[i], (float)zr[u].v[i], p.act);
         }
-        if (SUM) {
+        Run<T, 8, VEC> o;
 #pragma unroll
-          for (int i = 0; i < 8; ++i) sum[i] += dz[i];
+        for (int i = 0; i < 8; ++i) {
+          if (SUM) sum[i] += v[i];
+          o.v[i] = (T)v[i];
         }
-        store_run<T, 8>(static_cast<T*>(p.dz) + (s.begin + first + r0 + 4 * u) * p.n + col, nullptr, dz, left, vec);
+        o.store(dz + (int64_t)(r0 + 4 * u) * p.n, left);
       }
     }
   }
@@ -109,25 +133,26 @@ __global__ __launch_bounds__(256) void act_grad_kernel(ActGradLaunch p, int col_
 // db[g] = the partial sums of the group's row blocks. A column has kLanes threads, each with
 // every kLanes-th block in order; their sums are added in order. (A group with a third of
 // the rows has hundreds of blocks: one thread after them all was the longest part.)
-constexpr int kLanes = 16;
+constexpr int kLanes = 4;
 
 __global__ __launch_bounds__(64 * kLanes) void act_grad_sum_kernel(ActGradLaunch p, int col_tiles) {
   __shared__ float sums[kLanes][64];
   const int g = blockIdx.x / col_tiles, lane = threadIdx.x & 63, part = threadIdx.x >> 6;
   const int64_t col = (int64_t)(blockIdx.x % col_tiles) * 64 + lane;
-  int first = 0, blocks = (int)((p.rows + kActGradRows - 1) / kActGradRows);
+  const int each = p.block_rows;
+  int first = 0, blocks = (int)((p.rows + each - 1) / each);
   if (p.offsets) {
-    first = segment_tiles(p.offsets, g, p.rows, kActGradRows);
+    first = segment_tiles(p.offsets, g, p.rows, each);
     const int64_t c = clamp_row(p.offsets[g + 1], p.rows) - clamp_row(p.offsets[g], p.rows);
-    blocks = c > 0 ? (int)((c + kActGradRows - 1) / kActGradRows) : 0;
+    blocks = c > 0 ? (int)((c + each - 1) / each) : 0;
     // malformed offsets stay inside the workspace
-    const int most = (int)act_grad_blocks(p.rows, p.groups);
+    const int most = (int)act_grad_blocks(p.rows, p.groups, each);
     blocks = first >= most ? 0 : first + blocks > most ? most - first : blocks;
   }
   float sum = 0.0f;
   if (col < p.n) {
     const float* q = p.partials + (int64_t)first * p.n + col;
-#pragma unroll 4
+#pragma unroll 8
     for (int b = part; b < blocks; b += kLanes) sum += q[(int64_t)b * p.n];
   }
   sums[part][lane] = sum;
@@ -138,15 +163,28 @@ __global__ __launch_bounds__(64 * kLanes) void act_grad_sum_kernel(ActGradLaunch
   }
 }
 
+template <typename T, bool SUM, bool GATED>
+void launch_rows(const ActGradLaunch& a, dim3 grid, int col_tiles, hipStream_t st) {
+  if (a.n % 8 == 0)
+    act_grad_kernel<T, SUM, GATED, true><<<grid, 256, 0, st>>>(a, col_tiles);
+  else
+    act_grad_kernel<T, SUM, GATED, false><<<grid, 256, 0, st>>>(a, col_tiles);
+}
+
 template <typename T>
 hipError_t launch_t(const ActGradLaunch& a, hipStream_t st) {
-  const int64_t col_tiles = (a.n + kCols - 1) / kCols, blocks = act_grad_blocks(a.rows, a.groups);
+  const int64_t col_tiles = (a.n + kCols - 1) / kCols, blocks = act_grad_blocks(a.rows, a.groups, a.block_rows);
   if (blocks > 0) {
     const dim3 grid((uint32_t)(blocks * col_tiles));
-    if (a.db)
-      act_grad_kernel<T, true><<<grid, 256, 0, st>>>(a, (int)col_tiles);
+    const bool gated = a.act == kActSwiglu;
+    if (a.db && gated)
+      launch_rows<T, true, true>(a, grid, (int)col_tiles, st);
+    else if (a.db)
+      launch_rows<T, true, false>(a, grid, (int)col_tiles, st);
+    else if (gated)
+      launch_rows<T, false, true>(a, grid, (int)col_tiles, st);
     else
-      act_grad_kernel<T, false><<<grid, 256, 0, st>>>(a, (int)col_tiles);
+      launch_rows<T, false, false>(a, grid, (int)col_tiles, st);
   }
   if (a.db) {
     const int64_t sum_tiles = (a.n + 63) / 64;

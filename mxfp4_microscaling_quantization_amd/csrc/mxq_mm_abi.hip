@@ -136,7 +136,7 @@ mxq_status mxq_act_grad(const void* dy, const void* z, mxq_dtype dt, int64_t row
   if (n == 0 || n > kMaxDim || rows > kMaxDim || rows > ((int64_t)1 << 40) / n) return MXQ_ESHAPE;
   if (act == MXQ_ACT_SWIGLU && n % 2) return MXQ_ESHAPE;
   // the grids enumerate row blocks x column tiles and groups x column tiles
-  if (act_grad_blocks(rows, n_experts) * ((n + 511) / 512) >= kMaxGrid / 64 || n_experts * ((n + 63) / 64) >= kMaxGrid / 256)
+  if (act_grad_blocks(rows, n_experts, act_grad_rows(rows, n)) * ((n + 511) / 512) >= kMaxGrid / 64 || n_experts * ((n + 63) / 64) >= kMaxGrid / 256)
     return MXQ_ESHAPE;
   if (!aligned(dy, 16) || !aligned(z, 16) || !aligned(dz, 16) || !aligned(db, 16) || !aligned(workspace, 16) ||
       !aligned(offsets, 8))
@@ -153,12 +153,13 @@ mxq_status mxq_act_grad(const void* dy, const void* z, mxq_dtype dt, int64_t row
   l.dz = dz;
   l.db = db;
   l.partials = static_cast<float*>(workspace);
+  l.block_rows = act_grad_rows(rows, n);
   return from_hip(launch_act_grad(l, reinterpret_cast<hipStream_t>(stream)));
 }
 
 int64_t mxq_act_grad_workspace(int64_t rows, int64_t n, int64_t n_experts) {
   if (rows <= 0 || n <= 0 || n_experts < 1 || rows > kMaxDim || n > kMaxDim || n_experts > 4096) return 0;
-  return act_grad_blocks(rows, n_experts) * n * 4;
+  return act_grad_blocks(rows, n_experts, act_grad_rows(rows, n)) * n * 4;
 }
 
 }  // extern "C"

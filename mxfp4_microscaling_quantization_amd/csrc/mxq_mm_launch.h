@@ -56,13 +56,15 @@ struct ActGradLaunch {
   void* dz;
   float* db;
   float* partials;
+  int block_rows;
 };
 
-// Rows that one workgroup of the activation gradient sums, and the row blocks that any
-// split of the rows into groups has at most.
-constexpr int kActGradRows = 64;
-constexpr int64_t act_grad_blocks(int64_t rows, int64_t groups) {
-  return (rows + (kActGradRows - 1) * groups) / kActGradRows;
+// Rows that one workgroup of the activation gradient sums: few where there would be fewer
+// workgroups of many than the chip holds.
+constexpr int act_grad_rows(int64_t rows, int64_t n) { return rows * ((n + 511) / 512) < 128 * 1024 ? 16 : 128; }
+// The row blocks that any split of the rows into groups has at most.
+constexpr int64_t act_grad_blocks(int64_t rows, int64_t groups, int64_t each) {
+  return (rows + (each - 1) * groups) / each;
 }
 hipError_t launch_act_grad(const ActGradLaunch& a, hipStream_t st);
 

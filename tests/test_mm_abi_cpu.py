@@ -117,11 +117,11 @@ def test_act_grad_refusals(kw, status):
 def test_act_grad_workspace():
     ws = mxq.lib().mxq_act_grad_workspace
     assert ws(0, 8, 1) == 0 and ws(8, 0, 1) == 0 and ws(8, 8, 0) == 0 and ws(8, 8, 4097) == 0
-    # one row block per started 64 rows of every group: enough for any split
-    for rows, groups in ((1, 1), (64, 1), (65, 1), (300, 7), (5, 9)):
+    # one row of partial sums per started 128 rows of every group at least: enough for any split
+    for rows, groups in ((1, 1), (64, 1), (65, 1), (300, 7), (5, 9), (10 ** 6, 64)):
         blocks = ws(rows, 10, groups) // 40
-        assert blocks >= (rows + 63) // 64
-        assert blocks >= min(rows, groups) - 1 + (rows - min(rows, groups) + 1 + 63) // 64
+        assert blocks >= (rows + 127) // 128
+        assert blocks >= min(rows, groups) - 1 + (rows - min(rows, groups) + 1 + 127) // 128
 
 
 U8, F32 = torch.uint8, torch.float32
