@@ -183,16 +183,20 @@ hipError_t launch_waves(const MmLaunch& a, hipStream_t st) {
   return hipGetLastError();
 }
 
-// Up to 16 rows: 16 x 16 results of a workgroup. Waves split k: sixteen for a long one, four
-// where the workgroups alone fill the chip (us, MXFP4, one row; 4, 8, 16 waves):
-// 4096 x 14336 (n x k) 16.3, 12.2, 10.5; 4096 x 4096 5.9, 5.3, 5.6; 14336 x 4096 12.1, 13.4, 18.5.
+// Up to 16 rows. Where 16-column workgroups leave CUs idle, many waves split a long k; where
+// they fill the chip several times over, wider ones read A's rows for more columns and
+// pass over the chip fewer times (us, MXFP4, one row of n x k; 16 columns and 4, 8, 16 waves:
+// 4096 x 14336 16.3, 12.2, 10.5; 4096 x 4096 5.9, 5.3, 5.6; 16 columns and 4 waves, 32 and 8,
+// 64 and 4: 14336 x 4096 11.0, 10.1, 13.8; 28672 x 4096 19.8, 17.8, 17.0; 64 experts of
+// 4096 x 7168 for 512 rows 238, 206, 184.5, which is 5.4 TB/s).
 // More rows: 32 x 32 results, so that a row of A is read for 32 columns
 // (64 rows of 4096 x 4096: 9.0 us; 32 x 16 results 12.5, 64 x 32 11.3).
 template <bool A8, bool B8>
 hipError_t launch_rows(const MmLaunch& a, bool few, hipStream_t st) {
   if (!few) return launch_waves<A8, B8, 2, 2, 8, 2>(a, st);
   const int64_t tiles = (a.n + 15) / 16 * (a.offsets ? (a.rows < a.groups ? a.rows : a.groups) : 1);
-  if (tiles >= 768) return launch_waves<A8, B8, 1, 1, 4, 2>(a, st);
+  if (tiles >= 1536) return launch_waves<A8, B8, 1, 4, 4, 1>(a, st);
+  if (tiles >= 768) return launch_waves<A8, B8, 1, 2, 8, 1>(a, st);
   if (a.k > 8192) return launch_waves<A8, B8, 1, 1, 16, 2>(a, st);
   return launch_waves<A8, B8, 1, 1, 8, 2>(a, st);
 }

@@ -16,15 +16,18 @@ constexpr int kCUs = 256;  // of an MI355X; the tiles' LDS leaves room for one w
 // wave has read its last fragments, the loads spread over the steps. Fragments of the next
 // step are read from LDS while the matrix cores work on the current one; one barrier a
 // slot is all that the waves wait for.
-template <bool A8, bool B8, int MI, int NI, int WN, int R, bool WG>
+// Small tiles leave too few products between a fragment's read and its use: there KS = 2
+// groups of waves hold the same results and take two steps of every turn each; their
+// sums are added at the end, each group finishing half of the rows.
+template <bool A8, bool B8, int MI, int NI, int WN, int KS, int R, bool WG>
 struct Tile {
-  static constexpr int Waves = 2 * WN, Threads = 64 * Waves;
+  static constexpr int Waves = 2 * WN * KS, Threads = 64 * Waves;
   static constexpr int BM = 64 * MI, BN = 32 * NI * WN;
   static constexpr int ASlot = BM * 128, BSlot = BN * 128;
   static constexpr int Slot = ASlot + BSlot, SRing = R * Slot;                // offsets in LDS
   static constexpr int DA = ASlot / 1024 / Waves, DB = BSlot / 1024 / Waves;  // 1 KiB loads of a wave for a slot
   // loads of the slots after the one that a barrier waits for (the fewest that are certain)
-  static constexpr int Younger = (R - 2) * (A8 == B8 ? DA + DB : DA);
+  static constexpr int Younger = KS == 2 && A8 ? 0 : (R - 2) * (A8 == B8 ? DA + DB : DA);
   // scales: 16 bytes of a row cover a chunk of two turns; R chunks, loaded R / 2 ahead
   static constexpr int SRows = BM + BN, SChunk = SRows * 16, Ahead = R / 2;
   static constexpr int SLoads = SRows / 16 / Waves;  // 256-byte loads of a wave in a chunk (16 rows each)
@@ -33,6 +36,7 @@ struct Tile {
   static constexpr int Lds = XRing + (WG ? R * XSlot : 0);
   // 32 rows of every wave, parked for the epilogue from the second slot on
   static constexpr int ParkBytes = Waves * 32 * 32 * NI * 4;
+  static_assert(KS == 1 || (MI == 2 && DA == MI && DB == MI), "two groups: half of the rows and a load a part");
   static_assert(Slot + ParkBytes <= SRing, "the parked rows fit beside the first slot");
   static_assert(DA % 2 == 0 && DB % 2 == 0, "a wave's loads of a slot come in pairs");
 };
@@ -174,9 +178,9 @@ __device__ __forceinline__ int64_t list_entry(int64_t turn) {
   return turn * grid + x * q + (x < r ? x : r) + (blockIdx.x >> 3);
 }
 
-template <bool A8, bool B8, bool EXACT, int MI, int NI, int WN, int R, bool ODDK, bool WG, typename T>
-__global__ __launch_bounds__(128 * WN, MI *NI > 8 ? 1 : 2) void mm_tile_kernel(MmLaunch p, int col_tiles) {
-  using G = Tile<A8, B8, MI, NI, WN, R, WG>;
+template <bool A8, bool B8, bool EXACT, int MI, int NI, int WN, int KS, int R, bool ODDK, bool WG, typename T>
+__global__ __launch_bounds__(128 * WN * KS, MI *NI > 8 ? 1 : 2) void mm_tile_kernel(MmLaunch p, int col_tiles) {
+  using G = Tile<A8, B8, MI, NI, WN, KS, R, WG>;
   extern __shared__ __align__(16) uint8_t lds[];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r = lane & 31, h = lane >> 5;
@@ -341,7 +345,21 @@ __global__ __launch_bounds__(128 * WN, MI *NI > 8 ? 1 : 2) void mm_tile_kernel(M
   // The loads issued in step s of turn t, part u of MI of them: those of an FP8 slot in the
   // odd step that frees it and the step after, those of an MXFP4 slot in the last step and
   // the first two of the next turn (A's earlier than B's).
+  // Two groups: in the second step, which frees a turn's slots, and the first of the next.
   auto load_part = [&](int t, int s, int u) {
+    if constexpr (KS == 2) {
+      const int q8 = s ? 2 * t + R : 2 * t - 1 + R;
+      if (WG && u == 0) load_ninth(q8);
+      if (A8)
+        load_a(q8, u);
+      else if (s)
+        load_a(t + R, u);
+      if (B8)
+        load_b(q8, u);
+      else if (!s)
+        load_b(t - 1 + R, u);
+      return;
+    }
     if (WG && (s & 1) && u == 0) load_ninth(2 * t + (s + 1) / 2 - 1 + R);
     if constexpr (A8) {
 #pragma unroll
@@ -434,12 +452,14 @@ __global__ __launch_bounds__(128 * WN, MI *NI > 8 ? 1 : 2) void mm_tile_kernel(M
     barrier();
   };
 
-  const int wm = wave / WN, wn = wave % WN;
+  // kg: the wave's group; its steps of a turn are 2 kg and 2 kg + 1 where there are two
+  const int kg = KS == 2 ? wave / (2 * WN) : 0, wm = wave / WN % 2, wn = wave % WN;
   const int arow = wm * 32 * MI + r, brow = wn * 32 * NI + r;
-  int abase = frag_base<A8, EXACT>(arow, h), bbase = frag_base<B8, EXACT>(brow, h);
+  int abase = frag_base<A8, EXACT>(arow, h) ^ (A8 ? 0 : 64 * kg);
+  int bbase = frag_base<B8, EXACT>(brow, h) ^ (B8 ? 0 : 64 * kg);
   // Two FP8 fragment sets of A do not fit the registers: a fragment is then replaced by the
   // next step's as soon as its last product is issued.
-  constexpr bool Roll = A8 && B8 && !EXACT;
+  constexpr bool Roll = A8 && B8 && !EXACT && KS == 1;
   Frag<A8> fa[Roll ? 1 : 2][MI];
   Frag<B8> fb[2][NI];
   uint32_t sa[MI], sb[NI], ra[MI], rb[NI];
@@ -458,13 +478,13 @@ __global__ __launch_bounds__(128 * WN, MI *NI > 8 ? 1 : 2) void mm_tile_kernel(M
       }
   };
   auto read_a = [&](int t, int s, int i) {
-    Frag<A8> f = read_frag<A8, EXACT>(lds + ((A8 ? 2 * t + (s >> 1) : t) & (R - 1)) * G::Slot, abase, i, s);
-    if (WG && (s & 1) == 0) f.w[0] = merge_ninth(f.w[0], 2 * t + (s >> 1), row16(abase) + 512 * i);
+    Frag<A8> f = read_frag<A8, EXACT>(lds + ((A8 ? 2 * t + (s >> 1) + kg : t) & (R - 1)) * G::Slot, abase, i, s);
+    if (WG && (s & 1) == 0) f.w[0] = merge_ninth(f.w[0], 2 * t + (s >> 1) + kg, row16(abase) + 512 * i);
     return f;
   };
   // Fragments of step s of turn t: B's, and A's where they are not replaced one by one.
   auto read_step = [&](int t, int s) {
-    const uint8_t* b = lds + G::ASlot + ((B8 ? 2 * t + (s >> 1) : t) & (R - 1)) * G::Slot;
+    const uint8_t* b = lds + G::ASlot + ((B8 ? 2 * t + (s >> 1) + kg : t) & (R - 1)) * G::Slot;
     if constexpr (!Roll) {
 #pragma unroll
       for (int i = 0; i < MI; ++i) fa[s & 1][i] = read_a(t, s, i);
@@ -473,7 +493,7 @@ __global__ __launch_bounds__(128 * WN, MI *NI > 8 ? 1 : 2) void mm_tile_kernel(M
     for (int j = 0; j < NI; ++j) {
       fb[s & 1][j] = read_frag<B8, EXACT>(b, bbase, j, s);
       if (WG && (s & 1) == 0)
-        fb[s & 1][j].w[0] = merge_ninth(fb[s & 1][j].w[0], 2 * t + (s >> 1), 16 * G::BM + row16(bbase) + 512 * j);
+        fb[s & 1][j].w[0] = merge_ninth(fb[s & 1][j].w[0], 2 * t + (s >> 1) + kg, 16 * G::BM + row16(bbase) + 512 * j);
     }
   };
   // The scales of steps 2u and 2u + 1 as they lie in LDS; select_scales makes them the
@@ -511,7 +531,8 @@ __global__ __launch_bounds__(128 * WN, MI *NI > 8 ? 1 : 2) void mm_tile_kernel(M
 #pragma unroll
     for (int j = 0; j < G::DB; ++j) load_b(0, j);
   };
-  constexpr int PartA = A8 ? G::DA / 2 : G::DA < 3 ? G::DA : 3, PartB = B8 ? G::DB / 2 : 0;
+  constexpr int PartA = A8 ? (KS == 2 ? 0 : G::DA / 2) : G::DA < 3 ? G::DA : 3;
+  constexpr int PartB = B8 ? (KS == 2 ? 0 : G::DB / 2) : 0;
   auto start_rest = [&]() {
     if (WG && turns == 0) return;
 #pragma unroll
@@ -549,18 +570,58 @@ __global__ __launch_bounds__(128 * WN, MI *NI > 8 ? 1 : 2) void mm_tile_kernel(M
 #pragma unroll
       for (int j = 0; j < NI; ++j) c[i][j] = f32x16{};
     if (!WG || turns > 0) {
-      wait_loads<PartA + PartB + (R - 2) * (G::DA + G::DB)>();
+      wait_loads<KS == 2 && A8 ? G::DA + G::DB : PartA + PartB + (R - 2) * (G::DA + G::DB)>();
       barrier();
       if (ODDK && (tail & 1) && turns == 1) clear_tail();
-      if (WG && halves == 1) clear_group(0);
+      if (WG && (KS == 2 ? turns == 1 : halves == 1)) clear_group(halves - 1);
       read_step(0, 0);
       if constexpr (Roll) {
 #pragma unroll
         for (int i = 0; i < MI; ++i) fa[0][i] = read_a(0, 0, i);
       }
-      read_scales(0);
+      read_scales(kg);
       select_scales();
 
+      if constexpr (KS == 2) {
+        for (int t = 0; t + 1 < turns; ++t) {
+          asm volatile("" : "+v"(abase), "+v"(bbase));
+          if constexpr (WG) asm volatile("" : "+v"(keep_second));
+          if constexpr (ODDK) {
+            if ((t & 1) == 0 && t + 2 < turns) fetch_scales((t >> 1) + 1);
+            if ((t & 1) == 1) park_scales((t >> 1) + 1);
+          }
+          read_step(t, 1);
+          __builtin_amdgcn_sched_barrier(0);
+          multiply<A8, B8, EXACT, MI, NI>(c, fa[0], fb[0], sa, sb, 0, [&](int u) { load_part(t, 0, u); });
+          pin();
+          __builtin_amdgcn_sched_barrier(0);
+          // the next turn's slots have landed, and every wave has its last fragments of this one's
+          wait_loads<G::Younger>();
+          barrier();
+          if (WG && t + 2 == turns) clear_group(halves - 1);
+          if (ODDK && (tail & 1) && t + 2 == turns) clear_tail();
+          trim(t + R);
+          if constexpr (!ODDK)
+            if ((t & 1) == 0 && t + 2 * G::Ahead < turns) load_scales((t >> 1) + G::Ahead);
+          read_step(t + 1, 0);
+          read_scales(2 * t + 2 + kg);
+          __builtin_amdgcn_sched_barrier(0);
+          multiply<A8, B8, EXACT, MI, NI>(c, fa[1], fb[1], sa, sb, 1, [&](int u) { load_part(t, 1, u); });
+          pin();
+          __builtin_amdgcn_sched_barrier(0);
+          select_scales();
+        }
+        auto none = [](int) {};
+        if (last_steps > 2 * kg) {
+          if (last_steps > 2 * kg + 1) read_step(turns - 1, 1);
+          multiply<A8, B8, EXACT, MI, NI>(c, fa[0], fb[0], sa, sb, 0, none);
+          pin();
+          if (last_steps > 2 * kg + 1) {
+            multiply<A8, B8, EXACT, MI, NI>(c, fa[1], fb[1], sa, sb, 1, none);
+            pin();
+          }
+        }
+      } else {
       for (int t = 0; t + 1 < turns; ++t) {
         // addresses and masks are formed where used, not held
         asm volatile("" : "+v"(abase), "+v"(bbase));
@@ -610,6 +671,7 @@ __global__ __launch_bounds__(128 * WN, MI *NI > 8 ? 1 : 2) void mm_tile_kernel(M
           if (!ODDK || last_steps > 3) last_step(3);
         }
       }
+      }
     }
     // Every wave is done with the slots: the next tile's first loads start before this one's
     // results are finished and stored.
@@ -626,8 +688,36 @@ __global__ __launch_bounds__(128 * WN, MI *NI > 8 ? 1 : 2) void mm_tile_kernel(M
     float* park = reinterpret_cast<float*>(lds + G::Slot) + wave * 32 * 32 * NI;
     const int prow = lane / PerRow, pcol = lane % PerRow * V;
     RunEpilogue<T, V> out(p.ep, out_expert, out_col + pcol);
+    if constexpr (KS == 2) {
+      // each group hands the other the rows that that one finishes, and adds what it gets
+      float4* give = reinterpret_cast<float4*>(lds + G::Slot) + wave * 64 * 4 * NI + lane;
 #pragma unroll
-    for (int i = 0; i < MI; ++i) {
+      for (int j = 0; j < NI; ++j)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const f32x16& x = kg ? c[0][j] : c[1][j];
+          give[64 * (4 * j + q)] = make_float4(x[4 * q], x[4 * q + 1], x[4 * q + 2], x[4 * q + 3]);
+        }
+      wait_lds();
+      barrier();
+      const float4* take = reinterpret_cast<const float4*>(lds + G::Slot) + (wave ^ (2 * WN)) * 64 * 4 * NI + lane;
+#pragma unroll
+      for (int j = 0; j < NI; ++j)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const float4 y = take[64 * (4 * j + q)];
+          const f32x16& x = kg ? c[1][j] : c[0][j];
+          const f32x16 keep = x;
+          c[0][j][4 * q] = keep[4 * q] + y.x;
+          c[0][j][4 * q + 1] = keep[4 * q + 1] + y.y;
+          c[0][j][4 * q + 2] = keep[4 * q + 2] + y.z;
+          c[0][j][4 * q + 3] = keep[4 * q + 3] + y.w;
+        }
+      wait_lds();
+      barrier();
+    }
+#pragma unroll
+    for (int i = 0; i < (KS == 2 ? 1 : MI); ++i) {
 #pragma unroll
       for (int j = 0; j < NI; ++j)
 #pragma unroll
@@ -646,7 +736,7 @@ __global__ __launch_bounds__(128 * WN, MI *NI > 8 ? 1 : 2) void mm_tile_kernel(M
               z[v] = x.x, z[v + 1] = x.y, z[v + 2] = x.z, z[v + 3] = x.w;
             }
           },
-          out_row + 32 * i + prow, out_rows - 32 * i - prow);
+          out_row + 32 * (i + kg) + prow, out_rows - 32 * (i + kg) - prow);
       __builtin_amdgcn_wave_barrier();
     }
     if (!more) return;
@@ -655,14 +745,14 @@ __global__ __launch_bounds__(128 * WN, MI *NI > 8 ? 1 : 2) void mm_tile_kernel(M
   }
 }
 
-template <bool A8, bool B8, bool EXACT, int MI, int NI, int WN, int R, bool ODDK, bool WG, typename T>
+template <bool A8, bool B8, bool EXACT, int MI, int NI, int WN, int KS, int R, bool ODDK, bool WG, typename T>
 hipError_t launch_tile(const MmLaunch& a, hipStream_t st) {
-  using G = Tile<A8, B8, MI, NI, WN, R, WG>;
+  using G = Tile<A8, B8, MI, NI, WN, KS, R, WG>;
   const int64_t col_tiles = ((WG ? a.k : a.n) + G::BN - 1) / G::BN;
   const int64_t row_tiles = WG          ? (a.n + G::BM - 1) / G::BM * a.groups
                             : a.offsets ? a.rows / G::BM + (a.rows < a.groups ? a.rows : a.groups)
                                         : (a.rows + G::BM - 1) / G::BM;
-  auto k = mm_tile_kernel<A8, B8, EXACT, MI, NI, WN, R, ODDK, WG, T>;
+  auto k = mm_tile_kernel<A8, B8, EXACT, MI, NI, WN, KS, R, ODDK, WG, T>;
   static const hipError_t set =
       hipFuncSetAttribute(reinterpret_cast<const void*>(k), hipFuncAttributeMaxDynamicSharedMemorySize, G::Lds);
   if (set != hipSuccess) return set;
@@ -673,26 +763,26 @@ hipError_t launch_tile(const MmLaunch& a, hipStream_t st) {
 
 // Waves of 32 MI x 32 NI results, WN of them across; the exact product's need the registers
 // of a wave that has a SIMD for itself in the large tile (ENI, EWN).
-template <int MI, int NI, int WN, int ENI, int EWN, int R>
+template <int MI, int NI, int WN, int ENI, int EWN, int KS, int R>
 hipError_t launch_sized(const MmLaunch& a, hipStream_t st) {
   const bool f32 = a.ep.out_f32;
   if (a.a_fmt && a.b_fmt)
-    return f32 ? launch_tile<true, true, true, MI, ENI, EWN, R, false, false, float>(a, st)
-               : launch_tile<true, true, false, MI, NI, WN, R, false, false, __bf16>(a, st);
+    return f32 ? launch_tile<true, true, true, MI, ENI, EWN, KS, R, false, false, float>(a, st)
+               : launch_tile<true, true, false, MI, NI, WN, KS, R, false, false, __bf16>(a, st);
   if (a.a_fmt)
-    return f32 ? launch_tile<true, false, true, MI, ENI, EWN, R, false, false, float>(a, st)
-               : launch_tile<true, false, false, MI, NI, WN, R, false, false, __bf16>(a, st);
+    return f32 ? launch_tile<true, false, true, MI, ENI, EWN, KS, R, false, false, float>(a, st)
+               : launch_tile<true, false, false, MI, NI, WN, KS, R, false, false, __bf16>(a, st);
   if (a.k % 128)
-    return f32 ? launch_tile<false, false, false, MI, NI, WN, R, true, false, float>(a, st)
-               : launch_tile<false, false, false, MI, NI, WN, R, true, false, __bf16>(a, st);
-  return f32 ? launch_tile<false, false, false, MI, NI, WN, R, false, false, float>(a, st)
-             : launch_tile<false, false, false, MI, NI, WN, R, false, false, __bf16>(a, st);
+    return f32 ? launch_tile<false, false, false, MI, NI, WN, KS, R, true, false, float>(a, st)
+               : launch_tile<false, false, false, MI, NI, WN, KS, R, true, false, __bf16>(a, st);
+  return f32 ? launch_tile<false, false, false, MI, NI, WN, KS, R, false, false, float>(a, st)
+             : launch_tile<false, false, false, MI, NI, WN, KS, R, false, false, __bf16>(a, st);
 }
 
 }  // namespace
 
 hipError_t launch_gemm_tiles(const MmLaunch& a, bool large, hipStream_t st) {
-  return large ? launch_sized<4, 2, 4, 4, 2, 2>(a, st) : launch_sized<2, 1, 4, 1, 4, 4>(a, st);
+  return large ? launch_sized<4, 2, 4, 4, 2, 1, 2>(a, st) : launch_sized<2, 2, 2, 2, 2, 2, 4>(a, st);
 }
 
 bool large_tiles(int64_t rows, int64_t cols, int64_t extra_rows, int64_t each) {
@@ -705,10 +795,10 @@ bool large_tiles(int64_t rows, int64_t cols, int64_t extra_rows, int64_t each) {
 
 hipError_t launch_grouped_wgrad(const MmLaunch& a, hipStream_t st) {
   if (large_tiles(a.n - 1, a.k, 0, a.groups))
-    return a.ep.out_f32 ? launch_tile<true, true, true, 4, 4, 2, 2, false, true, float>(a, st)
-                        : launch_tile<true, true, false, 4, 2, 4, 2, false, true, __bf16>(a, st);
-  return a.ep.out_f32 ? launch_tile<true, true, true, 2, 1, 4, 4, false, true, float>(a, st)
-                      : launch_tile<true, true, false, 2, 1, 4, 4, false, true, __bf16>(a, st);
+    return a.ep.out_f32 ? launch_tile<true, true, true, 4, 4, 2, 1, 2, false, true, float>(a, st)
+                        : launch_tile<true, true, false, 4, 2, 4, 1, 2, false, true, __bf16>(a, st);
+  return a.ep.out_f32 ? launch_tile<true, true, true, 2, 2, 2, 2, 4, false, true, float>(a, st)
+                      : launch_tile<true, true, false, 2, 2, 2, 2, 4, false, true, __bf16>(a, st);
 }
 
 }  // namespace mxq
