@@ -633,23 +633,33 @@ __global__ __launch_bounds__(128 * WN * KS, MI *NI > 8 ? 1 : 2) void mm_tile_ker
         }
 #pragma unroll
         for (int s = 0; s < 4; ++s) {
-          // the next slots have landed, and every wave has its last fragments of the current ones
-          if (s == 3 || (s == 1 && (A8 || B8))) {
-            wait_loads<G::Younger>();
-            barrier();
-            if (WG && s == 3 && t + 2 == turns && (halves & 1)) clear_group(halves - 1);
-          }
-          if (s == 3) {
-            if (ODDK && (tail & 1) && t + 2 == turns) clear_tail();
-            trim(t + R);
-            if constexpr (!ODDK)
-              if ((t & 1) == 0 && t + 2 * G::Ahead < turns) load_scales((t >> 1) + G::Ahead);
-          }
           const int tn = s == 3 ? t + 1 : t, sn = (s + 1) & 3;
-          read_step(tn, sn);
-          if (s & 1) read_scales(2 * t + (s + 1) / 2);
+          auto advance = [&]() {
+            // the next slots have landed, and every wave has its last fragments of the current ones
+            if (s == 3 || (s == 1 && (A8 || B8))) {
+              wait_loads<G::Younger>();
+              barrier();
+              if (WG && s == 3 && t + 2 == turns && (halves & 1)) clear_group(halves - 1);
+            }
+            if (s == 3) {
+              if (ODDK && (tail & 1) && t + 2 == turns) clear_tail();
+              trim(t + R);
+              if constexpr (!ODDK)
+                if ((t & 1) == 0 && t + 2 * G::Ahead < turns) load_scales((t >> 1) + G::Ahead);
+            }
+            read_step(tn, sn);
+            if (s & 1) read_scales(2 * t + (s + 1) / 2);
+          };
+          // Where A's fragments are replaced one by one, the last of them has just been read: its
+          // step's first products go ahead of the wait.
+          const bool late = Roll && !WG && (s & 1);  // (the weight gradient's registers do not allow it)
+          if (!late) advance();
           __builtin_amdgcn_sched_barrier(0);
           multiply<A8, B8, EXACT, MI, NI>(c, fa[Roll ? 0 : s & 1], fb[s & 1], sa, sb, s & 1, [&](int u) {
+            if (late && u == 0) {
+              pin();
+              advance();
+            }
             if constexpr (Roll) fa[0][u] = read_a(tn, sn, u);
             load_part(t, s, u);
           });

@@ -157,3 +157,15 @@ def cpu(shape, dtype=U8):
 def test_binding_refusals(call, error):
     with pytest.raises(error):
         call()
+
+
+def test_header_is_plain_c(tmp_path):
+    """include/mxq_gemm.h compiles as C and as C++ by itself."""
+    import shutil
+    import subprocess
+    src = tmp_path / "t.c"
+    src.write_text('#include "mxq_gemm.h"\nint main(void) { return MXQ_ACT_SWIGLU - 4 + MXQ_OPERAND_MXFP4; }\n')
+    for cc, std in (("gcc", "-std=c99"), ("g++", "-std=c++11")):
+        if shutil.which(cc):
+            subprocess.run([cc, std, "-Wall", "-Werror", "-x", "c" if cc == "gcc" else "c++", "-fsyntax-only", "-I",
+                            os.path.join(ROOT, "include"), str(src)], check=True)
