@@ -246,20 +246,26 @@ struct RunEpilogue {
     }
   }
 
+  // (one uniform branch around all elements: a branch in each cost 45 us of 310 at
+  // 8192 x 14336 results)
   template <int U>
   static __device__ __forceinline__ void act_runs(float (&v)[U][V], int act) {
-    if (act == kActNone) return;
+    if (act == kActRelu) {
 #pragma unroll
-    for (int k = 0; k < U; ++k)
+      for (int k = 0; k < U; ++k)
 #pragma unroll
-      for (int i = 0; i < V; ++i) {
-        if (act == kActRelu)
-          v[k][i] = v[k][i] < 0.0f ? 0.0f : v[k][i];
-        else if (act == kActGelu)
-          v[k][i] = gelu_f(v[k][i]);
-        else
-          v[k][i] = v[k][i] * sigmoid_f(v[k][i]);
-      }
+        for (int i = 0; i < V; ++i) v[k][i] = v[k][i] < 0.0f ? 0.0f : v[k][i];
+    } else if (act == kActGelu) {
+#pragma unroll
+      for (int k = 0; k < U; ++k)
+#pragma unroll
+        for (int i = 0; i < V; ++i) v[k][i] = gelu_f(v[k][i]);
+    } else if (act == kActSilu) {
+#pragma unroll
+      for (int k = 0; k < U; ++k)
+#pragma unroll
+        for (int i = 0; i < V; ++i) v[k][i] *= sigmoid_f(v[k][i]);
+    }
   }
 };
 
