@@ -152,59 +152,65 @@ __device__ __forceinline__ void epilogue_run(const MmEpilogue& ep, int64_t row, 
 }
 
 // The same for one lane that finishes V fixed columns of many rows from sums in LDS:
-// bias, addresses and strides are set up once, and four rows are in flight together.
+// bias, addresses and strides are set up once, four rows are in flight together, and the
+// residual's next four are fetched before these are stored.
 template <typename T, int V>
 struct RunEpilogue {
+  static constexpr int U = 4;
   float bias[V];
-  int64_t n0, dn, dcol;
-  int left;
+  int64_t at;      // of the next row's results in d (in z twice that where half of d's columns are left)
+  int left, rows;  // columns; rows from the next one on
   bool vec, gated;
+  T raw[U][V] = {};
 
-  __device__ __forceinline__ RunEpilogue(const MmEpilogue& ep, int group, int64_t first) : n0(first) {
+  // Rows first, first + STEP, ... below first + `rows` of columns col...
+  template <int STEP>
+  __device__ __forceinline__ void start(const MmEpilogue& ep, int64_t col, int64_t first, int to_do) {
     gated = ep.act == kActSwiglu;
-    dn = gated ? ep.n / 2 : ep.n;
-    dcol = gated ? first / 2 : first;
-    left = ep.n - first < V ? (int)(ep.n - first) : V;
+    at = first * row_step(ep) + (gated ? col / 2 : col);
+    left = ep.n - col < V ? (int)(ep.n - col) : V;
+    rows = left > 0 ? to_do : 0;
     vec = ep.n % V == 0;
+    if (ep.res && vec) fetch<STEP>(ep, 0);
+  }
+
+  __device__ __forceinline__ void fetch_bias(const MmEpilogue& ep, int group, int64_t col) {
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       bias[i] = 0.0f;
       if (ep.bias && i < left) {
-        const int64_t at = (int64_t)group * ep.n + first + i;
-        bias[i] = ep.bias_f32 ? static_cast<const float*>(ep.bias)[at] : (float)static_cast<const __bf16*>(ep.bias)[at];
+        const int64_t b = (int64_t)group * ep.n + col + i;
+        bias[i] = ep.bias_f32 ? static_cast<const float*>(ep.bias)[b] : (float)static_cast<const __bf16*>(ep.bias)[b];
       }
     }
   }
 
-  // N rows `row`, row + STEP, ... (those from `rows` on missing), whose sums get(k, z) fetches.
+  __device__ __forceinline__ int64_t row_step(const MmEpilogue& ep) const { return gated ? ep.n / 2 : ep.n; }
+
+  // The residual's rows `from`, from + 1, ... of those to come.
+  template <int STEP>
+  __device__ __forceinline__ void fetch(const MmEpilogue& ep, int from) {
+    const int64_t step = STEP * row_step(ep);
+    const T* p = static_cast<const T*>(ep.res) + at + from * step;
+#pragma unroll
+    for (int k = 0; k < U; ++k)
+      if ((from + k) * STEP < rows) {
+        if (gated)
+          __builtin_memcpy(raw[k], __builtin_assume_aligned(p + k * step, (kRunAlign<T, V / 2>)), sizeof(T) * V / 2);
+        else
+          __builtin_memcpy(raw[k], __builtin_assume_aligned(p + k * step, (kRunAlign<T, V>)), sizeof(T) * V);
+      }
+  }
+
+  // The next N rows, whose sums get(k, z) fetches.
   template <int N, int STEP, typename F>
-  __device__ __forceinline__ void rows(const MmEpilogue& ep, F&& get, int64_t row, int rows) {
-    constexpr int U = N < 4 ? N : 4;
-    if (left <= 0) return;
-    T* d = static_cast<T*>(ep.d) + row * dn + dcol;
-    const T* res = static_cast<const T*>(ep.res) + row * dn + dcol;
-    T* keep = static_cast<T*>(ep.z) + row * ep.n + n0;
-    const int64_t dstep = STEP * dn, kstep = STEP * ep.n;
+  __device__ __forceinline__ void finish(const MmEpilogue& ep, F&& get) {
+    const int64_t step = STEP * row_step(ep);
 #pragma unroll 1
     for (int u = 0; u < N; u += U) {
-      float v[U][V], r[U][V];
+      float v[U][V];
 #pragma unroll
       for (int k = 0; k < U; ++k) get(u + k, v[k]);
-      if (ep.res && vec) {
-#pragma unroll
-        for (int k = 0; k < U; ++k) {
-          if ((u + k) * STEP < rows) {
-            if (gated) {
-              float half[V / 2];
-              get_run<T, V / 2>(res + k * dstep, half);
-#pragma unroll
-              for (int i = 0; i < V / 2; ++i) r[k][i] = half[i];
-            } else {
-              get_run<T, V>(res + k * dstep, r[k]);
-            }
-          }
-        }
-      }
       if (ep.bias) {
 #pragma unroll
         for (int k = 0; k < U; ++k)
@@ -212,43 +218,51 @@ struct RunEpilogue {
           for (int i = 0; i < V; ++i) v[k][i] += bias[i];
       }
       if (ep.z) {
+        T* z = static_cast<T*>(ep.z) + (gated ? 2 * at : at);
 #pragma unroll
         for (int k = 0; k < U; ++k)
-          if ((u + k) * STEP < rows) store_run<T, V>(keep + k * kstep, nullptr, v[k], left, vec);
+          if (k * STEP < rows) store_run<T, V>(z + k * (STEP * ep.n), nullptr, v[k], left, vec);
       }
       if (gated) {
 #pragma unroll
-        for (int k = 0; k < U; ++k) {
-          float g[V / 2];
+        for (int k = 0; k < U; ++k)
 #pragma unroll
-          for (int i = 0; i < V / 2; ++i) {
-            g[i] = v[k][2 * i] * sigmoid_f(v[k][2 * i]) * v[k][2 * i + 1];
-            if (ep.res && vec) g[i] += r[k][i];
-          }
-          if ((u + k) * STEP < rows)
-            store_run<T, V / 2>(d + k * dstep, vec || !ep.res ? nullptr : res + k * dstep, g, left / 2, vec);
-        }
+          for (int i = 0; i < V / 2; ++i) v[k][i] = v[k][2 * i] * sigmoid_f(v[k][2 * i]) * v[k][2 * i + 1];
       } else {
-        act_runs<U>(v, ep.act);
+        act_runs(v, ep.act);
+      }
+      const T* rest = nullptr;
+      if (ep.res && vec) {
 #pragma unroll
-        for (int k = 0; k < U; ++k) {
-          if (ep.res && vec) {
+        for (int k = 0; k < U; ++k)
 #pragma unroll
-            for (int i = 0; i < V; ++i) v[k][i] += r[k][i];
+          for (int i = 0; i < V; ++i) v[k][i] += Out<T>::get(&raw[k][i]);  // (gated: half of them count)
+        fetch<STEP>(ep, U);
+      } else if (ep.res) {
+        rest = static_cast<const T*>(ep.res) + at;
+      }
+      T* d = static_cast<T*>(ep.d) + at;
+#pragma unroll
+      for (int k = 0; k < U; ++k) {
+        const T* from = rest ? rest + k * step : nullptr;
+        if (k * STEP < rows) {
+          if (gated) {
+            float g[V / 2];
+#pragma unroll
+            for (int i = 0; i < V / 2; ++i) g[i] = v[k][i];
+            store_run<T, V / 2>(d + k * step, from, g, left / 2, vec);
+          } else {
+            store_run<T, V>(d + k * step, from, v[k], left, vec);
           }
-          if ((u + k) * STEP < rows)
-            store_run<T, V>(d + k * dstep, vec || !ep.res ? nullptr : res + k * dstep, v[k], left, vec);
         }
       }
-      d += U * dstep;
-      res += U * dstep;
-      keep += U * kstep;
+      at += U * step;
+      rows -= U * STEP;
     }
   }
 
   // (one uniform branch around all elements: a branch in each cost 45 us of 310 at
   // 8192 x 14336 results)
-  template <int U>
   static __device__ __forceinline__ void act_runs(float (&v)[U][V], int act) {
     if (act == kActRelu) {
 #pragma unroll

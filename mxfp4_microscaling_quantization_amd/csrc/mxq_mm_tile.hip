@@ -684,20 +684,24 @@ __global__ __launch_bounds__(128 * WN * KS, MI *NI > 8 ? 1 : 2) void mm_tile_ker
       }
     }
     // Every wave is done with the slots: the next tile's first loads start before this one's
-    // results are finished and stored.
+    // results are finished and stored, 32 rows at a time through LDS, so that rows leave as
+    // whole runs.
     wait_loads<0>();
     barrier();
-    const int64_t out_row = orow0 + wm * 32 * MI, out_col = col0 + wn * 32 * NI;
-    const int out_rows = arows - wm * 32 * MI, out_expert = expert;
-    const bool more = set_up(list_entry(entry + 1));
-    if (more) start_first();
-
-    // Epilogue: 32 rows at a time through LDS, so that rows leave as whole runs.
     constexpr int V = sizeof(T) == 2 ? 8 : 4, PerRow = 32 * NI / V, RowsAtOnce = 64 / PerRow;
     constexpr int Pieces = 8 * NI;  // 16-byte pieces of a parked row, exchanged so that no read or write collides
     float* park = reinterpret_cast<float*>(lds + G::Slot) + wave * 32 * 32 * NI;
     const int prow = lane / PerRow, pcol = lane % PerRow * V;
-    RunEpilogue<T, V> out(p.ep, out_expert, out_col + pcol);
+    const int64_t out_row = orow0 + 32 * (wm * MI + kg) + prow;
+    constexpr int WaveRows = KS == 2 ? 32 : 32 * MI;
+    const int left = arows - 32 * (wm * MI + kg), out_rows = (left < WaveRows ? left : WaveRows) - prow;
+    RunEpilogue<T, V> out;
+    const int64_t out_col = col0 + wn * 32 * NI + pcol;
+    const int out_expert = expert;
+    out.template start<RowsAtOnce>(p.ep, out_col, out_row, out_rows);
+    const bool more = set_up(list_entry(entry + 1));
+    if (more) start_first();
+    out.fetch_bias(p.ep, out_expert, out_col);
     if constexpr (KS == 2) {
       // each group hands the other the rows that that one finishes, and adds what it gets
       float4* give = reinterpret_cast<float4*>(lds + G::Slot) + wave * 64 * 4 * NI + lane;
@@ -735,9 +739,8 @@ __global__ __launch_bounds__(128 * WN * KS, MI *NI > 8 ? 1 : 2) void mm_tile_ker
           *reinterpret_cast<float4*>(park + r * 32 * NI + 4 * ((8 * j + 2 * q + h) ^ (r & (Pieces - 1)))) =
               make_float4(c[i][j][4 * q], c[i][j][4 * q + 1], c[i][j][4 * q + 2], c[i][j][4 * q + 3]);
       __builtin_amdgcn_wave_barrier();
-      out.template rows<32 / RowsAtOnce, RowsAtOnce>(
-          p.ep,
-          [&](int k, float(&z)[V]) {
+      out.template finish<32 / RowsAtOnce, RowsAtOnce>(
+          p.ep, [&](int k, float(&z)[V]) {
             const int row = prow + k * RowsAtOnce;
 #pragma unroll
             for (int v = 0; v < V; v += 4) {
@@ -745,8 +748,7 @@ __global__ __launch_bounds__(128 * WN * KS, MI *NI > 8 ? 1 : 2) void mm_tile_ker
                   park + row * 32 * NI + 4 * ((pcol / 4 + v / 4) ^ (row & (Pieces - 1))));
               z[v] = x.x, z[v + 1] = x.y, z[v + 2] = x.z, z[v + 3] = x.w;
             }
-          },
-          out_row + 32 * (i + kg) + prow, out_rows - 32 * (i + kg) - prow);
+          });
       __builtin_amdgcn_wave_barrier();
     }
     if (!more) return;
