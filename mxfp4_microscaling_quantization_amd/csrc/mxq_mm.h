@@ -152,11 +152,10 @@ __device__ __forceinline__ void epilogue_run(const MmEpilogue& ep, int64_t row, 
 }
 
 // The same for one lane that finishes V fixed columns of many rows from sums in LDS:
-// bias, addresses and strides are set up once, four rows are in flight together, and the
-// residual's next four are fetched before these are stored.
-template <typename T, int V>
+// bias, addresses and strides are set up once, U rows are in flight together, and the
+// residual's next U are fetched before these are stored.
+template <typename T, int V, int U>
 struct RunEpilogue {
-  static constexpr int U = 4;
   float bias[V];
   int64_t at;      // of the next row's results in d (in z twice that where half of d's columns are left)
   int left, rows;  // columns; rows from the next one on

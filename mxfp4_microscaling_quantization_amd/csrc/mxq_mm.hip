@@ -4,14 +4,19 @@
 namespace mxq {
 
 // Which kernel. Few rows: the weight streams past them (rows kernel; an expert's share of
-// the tokens stands for its rows). With 17 to 64 rows that holds while the 128-column tiles
-// are few (64 rows of n x k, rows kernel and tiles, us: 4096 x 4096 9.0 and 13.6, 14336 x 4096
-// 31.7 and 16.6). Otherwise tiles, see large_tiles.
+// the tokens stands for its rows). With 17 to 64 rows that holds while its workgroups of
+// 32 x 32 results all run at once, one on each of the 256 CUs (MXFP4, k 4096, rows kernel and
+// tiles, us: 64 x 4096 results 8.8 and 10.4, 64 x 6144 16.2 and 10.7, 32 x 8192 9.2 and 10.8),
+// but not for FP8 products that may take the FP8 matrix instructions, which the rows kernel
+// does without (64 x 4096: 16.2 and 11.8), and not for experts, whose rows are uneven (8
+// experts, 384 tokens, 4096 x 4096: 62.6 and 19.7).
 hipError_t launch_gemm(const MmLaunch& a, hipStream_t st) {
   const int64_t each = a.offsets ? (a.rows + a.groups - 1) / a.groups : a.rows;
-  if (each <= 16 || (each <= 64 && a.n < 8192)) return launch_gemm_rows(a, each <= 16, st);
-  const bool large = a.offsets ? large_tiles(a.rows, a.n, a.groups / 2, 1) : large_tiles(a.rows - 1, a.n, 0, 1);
-  return launch_gemm_tiles(a, large, st);
+  const bool at_once = (a.rows + 31) / 32 * ((a.n + 31) / 32) <= 256;
+  const bool fp8 = a.a_fmt && a.b_fmt && !a.ep.out_f32;
+  if (each <= 16 || (each <= 64 && !a.offsets && at_once && !fp8)) return launch_gemm_rows(a, each <= 16, st);
+  const int side = a.offsets ? tile_side(a.rows, a.n, a.groups / 2, 1) : tile_side(a.rows - 1, a.n, 0, 1);
+  return launch_gemm_tiles(a, side, st);
 }
 
 }  // namespace mxq

@@ -16,9 +16,12 @@ constexpr int kCUs = 256;  // of an MI355X; the tiles' LDS leaves room for one w
 // wave has read its last fragments, the loads spread over the steps. Fragments of the next
 // step are read from LDS while the matrix cores work on the current one; one barrier a
 // slot is all that the waves wait for.
-// Small tiles leave too few products between a fragment's read and its use: there KS = 2
-// groups of waves hold the same results and take two steps of every turn each; their
-// sums are added at the end, each group finishing half of the rows.
+// Tiles of 128 leave few products between a fragment's read and its use: there, except for
+// FP8 instructions (512 x 14336 x 4096: 50 us with two groups, 44 with one), KS = 2 groups of
+// waves hold the same results and take two steps of every turn each; their sums are added
+// at the end, each group finishing half of the rows. Tiles of 64 leave room for a second
+// workgroup on the CU instead (and gained nothing from a ring of eight slots, and up to a
+// tenth from two groups at FP4).
 template <bool A8, bool B8, int MI, int NI, int WN, int KS, int R, bool WG>
 struct Tile {
   static constexpr int Waves = 2 * WN * KS, Threads = 64 * Waves;
@@ -133,8 +136,9 @@ __device__ __forceinline__ f32x16 multiply_scaled(const Frag<A8>& a, const Frag<
                                                          B8 ? 0 : 2, (int)sb, A8 ? 0 : 2, (int)sa);
 }
 
-// One step on the matrix cores, the first (step 0) or second of a scale register's two. `between` is called MI times in the course of it
-// (with 0 .. MI - 1) to issue loads while the matrix cores are busy.
+// One step on the matrix cores, the first (step 0) or second of a scale register's two.
+// `between` is called MI times in the course of it (with 0 .. MI - 1) to issue loads while
+// the matrix cores are busy.
 template <bool A8, bool B8, bool EXACT, int MI, int NI, typename F>
 __device__ __forceinline__ void multiply(f32x16 (&c)[MI][NI], const Frag<A8> (&a)[MI], const Frag<B8> (&b)[NI],
                                          const uint32_t (&sa)[MI], const uint32_t (&sb)[NI], int step, F&& between) {
@@ -179,7 +183,7 @@ __device__ __forceinline__ int64_t list_entry(int64_t turn) {
 }
 
 template <bool A8, bool B8, bool EXACT, int MI, int NI, int WN, int KS, int R, bool ODDK, bool WG, typename T>
-__global__ __launch_bounds__(128 * WN * KS, MI *NI > 8 ? 1 : 2) void mm_tile_kernel(MmLaunch p, int col_tiles) {
+__global__ __launch_bounds__(128 * WN * KS, MI * NI > 8 ? 1 : 2) void mm_tile_kernel(MmLaunch p, int col_tiles) {
   using G = Tile<A8, B8, MI, NI, WN, KS, R, WG>;
   extern __shared__ __align__(16) uint8_t lds[];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -459,7 +463,7 @@ __global__ __launch_bounds__(128 * WN * KS, MI *NI > 8 ? 1 : 2) void mm_tile_ker
   int bbase = frag_base<B8, EXACT>(brow, h) ^ (B8 ? 0 : 64 * kg);
   // Two FP8 fragment sets of A do not fit the registers: a fragment is then replaced by the
   // next step's as soon as its last product is issued.
-  constexpr bool Roll = A8 && B8 && !EXACT && KS == 1;
+  constexpr bool Roll = A8 && B8 && !EXACT && KS == 1 && MI > 2;
   Frag<A8> fa[Roll ? 1 : 2][MI];
   Frag<B8> fb[2][NI];
   uint32_t sa[MI], sb[NI], ra[MI], rb[NI];
@@ -622,65 +626,65 @@ __global__ __launch_bounds__(128 * WN * KS, MI *NI > 8 ? 1 : 2) void mm_tile_ker
           }
         }
       } else {
-      for (int t = 0; t + 1 < turns; ++t) {
-        // addresses and masks are formed where used, not held
-        asm volatile("" : "+v"(abase), "+v"(bbase));
-        if constexpr (WG) asm volatile("" : "+v"(keep_second));
-        if constexpr (ODDK) {
-          // chunk c + 1 is fetched in the first turn of chunk c and parked in the second
-          if ((t & 1) == 0 && t + 2 < turns) fetch_scales((t >> 1) + 1);
-          if ((t & 1) == 1 && t + 1 < turns) park_scales((t >> 1) + 1);
-        }
+        for (int t = 0; t + 1 < turns; ++t) {
+          // addresses and masks are formed where used, not held
+          asm volatile("" : "+v"(abase), "+v"(bbase));
+          if constexpr (WG) asm volatile("" : "+v"(keep_second));
+          if constexpr (ODDK) {
+            // chunk c + 1 is fetched in the first turn of chunk c and parked in the second
+            if ((t & 1) == 0 && t + 2 < turns) fetch_scales((t >> 1) + 1);
+            if ((t & 1) == 1 && t + 1 < turns) park_scales((t >> 1) + 1);
+          }
 #pragma unroll
-        for (int s = 0; s < 4; ++s) {
-          const int tn = s == 3 ? t + 1 : t, sn = (s + 1) & 3;
-          auto advance = [&]() {
-            // the next slots have landed, and every wave has its last fragments of the current ones
-            if (s == 3 || (s == 1 && (A8 || B8))) {
-              wait_loads<G::Younger>();
-              barrier();
-              if (WG && s == 3 && t + 2 == turns && (halves & 1)) clear_group(halves - 1);
-            }
-            if (s == 3) {
-              if (ODDK && (tail & 1) && t + 2 == turns) clear_tail();
-              trim(t + R);
-              if constexpr (!ODDK)
-                if ((t & 1) == 0 && t + 2 * G::Ahead < turns) load_scales((t >> 1) + G::Ahead);
-            }
-            read_step(tn, sn);
-            if (s & 1) read_scales(2 * t + (s + 1) / 2);
-          };
-          // Where A's fragments are replaced one by one, the last of them has just been read: its
-          // step's first products go ahead of the wait.
-          const bool late = Roll && !WG && (s & 1);  // (the weight gradient's registers do not allow it)
-          if (!late) advance();
-          __builtin_amdgcn_sched_barrier(0);
-          multiply<A8, B8, EXACT, MI, NI>(c, fa[Roll ? 0 : s & 1], fb[s & 1], sa, sb, s & 1, [&](int u) {
-            if (late && u == 0) {
-              pin();
-              advance();
-            }
-            if constexpr (Roll) fa[0][u] = read_a(tn, sn, u);
-            load_part(t, s, u);
-          });
-          pin();
-          __builtin_amdgcn_sched_barrier(0);
-          if (s & 1) select_scales();
+          for (int s = 0; s < 4; ++s) {
+            const int tn = s == 3 ? t + 1 : t, sn = (s + 1) & 3;
+            auto advance = [&]() {
+              // the next slots have landed, and every wave has its last fragments of the current ones
+              if (s == 3 || (s == 1 && (A8 || B8))) {
+                wait_loads<G::Younger>();
+                barrier();
+                if (WG && s == 3 && t + 2 == turns && (halves & 1)) clear_group(halves - 1);
+              }
+              if (s == 3) {
+                if (ODDK && (tail & 1) && t + 2 == turns) clear_tail();
+                trim(t + R);
+                if constexpr (!ODDK)
+                  if ((t & 1) == 0 && t + 2 * G::Ahead < turns) load_scales((t >> 1) + G::Ahead);
+              }
+              read_step(tn, sn);
+              if (s & 1) read_scales(2 * t + (s + 1) / 2);
+            };
+            // Where A's fragments are replaced one by one, the last of them has just been read: its
+            // step's first products go ahead of the wait.
+            const bool late = Roll && !WG && (s & 1);  // (the weight gradient's registers do not allow it)
+            if (!late) advance();
+            __builtin_amdgcn_sched_barrier(0);
+            multiply<A8, B8, EXACT, MI, NI>(c, fa[Roll ? 0 : s & 1], fb[s & 1], sa, sb, s & 1, [&](int u) {
+              if (late && u == 0) {
+                pin();
+                advance();
+              }
+              if constexpr (Roll) fa[0][u] = read_a(tn, sn, u);
+              load_part(t, s, u);
+            });
+            pin();
+            __builtin_amdgcn_sched_barrier(0);
+            if (s & 1) select_scales();
+          }
         }
-      }
-      last_step(0);
-      if (!ODDK || last_steps > 1) {
-        if constexpr (A8 || B8) {
-          wait_loads<G::Younger>();
-          barrier();
-          if (WG && 2 * turns == halves) clear_group(halves - 1);
+        last_step(0);
+        if (!ODDK || last_steps > 1) {
+          if constexpr (A8 || B8) {
+            wait_loads<G::Younger>();
+            barrier();
+            if (WG && 2 * turns == halves) clear_group(halves - 1);
+          }
+          last_step(1);
+          if (last_steps > 2) {
+            last_step(2);
+            if (!ODDK || last_steps > 3) last_step(3);
+          }
         }
-        last_step(1);
-        if (last_steps > 2) {
-          last_step(2);
-          if (!ODDK || last_steps > 3) last_step(3);
-        }
-      }
       }
     }
     // Every wave is done with the slots: the next tile's first loads start before this one's
@@ -692,10 +696,12 @@ __global__ __launch_bounds__(128 * WN * KS, MI *NI > 8 ? 1 : 2) void mm_tile_ker
     constexpr int Pieces = 8 * NI;  // 16-byte pieces of a parked row, exchanged so that no read or write collides
     float* park = reinterpret_cast<float*>(lds + G::Slot) + wave * 32 * 32 * NI;
     const int prow = lane / PerRow, pcol = lane % PerRow * V;
-    const int64_t out_row = orow0 + 32 * (wm * MI + kg) + prow;
-    constexpr int WaveRows = KS == 2 ? 32 : 32 * MI;
-    const int left = arows - 32 * (wm * MI + kg), out_rows = (left < WaveRows ? left : WaveRows) - prow;
-    RunEpilogue<T, V> out;
+    const int64_t out_row = orow0 + 32 * MI * wm + 32 * MI / KS * kg + prow;
+    // (two groups: each finishes half of the rows)
+    constexpr int WaveRows = 32 * MI / KS;
+    const int left = arows - 32 * MI * wm - WaveRows * kg, out_rows = (left < WaveRows ? left : WaveRows) - prow;
+    constexpr int Runs = 32 / RowsAtOnce;
+    RunEpilogue<T, V, (Runs < 4 ? Runs : 4)> out;
     const int64_t out_col = col0 + wn * 32 * NI + pcol;
     const int out_expert = expert;
     out.template start<RowsAtOnce>(p.ep, out_col, out_row, out_rows);
@@ -739,16 +745,15 @@ __global__ __launch_bounds__(128 * WN * KS, MI *NI > 8 ? 1 : 2) void mm_tile_ker
           *reinterpret_cast<float4*>(park + r * 32 * NI + 4 * ((8 * j + 2 * q + h) ^ (r & (Pieces - 1)))) =
               make_float4(c[i][j][4 * q], c[i][j][4 * q + 1], c[i][j][4 * q + 2], c[i][j][4 * q + 3]);
       __builtin_amdgcn_wave_barrier();
-      out.template finish<32 / RowsAtOnce, RowsAtOnce>(
-          p.ep, [&](int k, float(&z)[V]) {
-            const int row = prow + k * RowsAtOnce;
+      out.template finish<Runs, RowsAtOnce>(p.ep, [&](int k, float(&z)[V]) {
+        const int row = prow + k * RowsAtOnce;
 #pragma unroll
-            for (int v = 0; v < V; v += 4) {
-              const float4 x = *reinterpret_cast<const float4*>(
-                  park + row * 32 * NI + 4 * ((pcol / 4 + v / 4) ^ (row & (Pieces - 1))));
-              z[v] = x.x, z[v + 1] = x.y, z[v + 2] = x.z, z[v + 3] = x.w;
-            }
-          });
+        for (int v = 0; v < V; v += 4) {
+          const int at = row * 32 * NI + 4 * ((pcol / 4 + v / 4) ^ (row & (Pieces - 1)));
+          const float4 x = *reinterpret_cast<const float4*>(park + at);
+          z[v] = x.x, z[v + 1] = x.y, z[v + 2] = x.z, z[v + 3] = x.w;
+        }
+      });
       __builtin_amdgcn_wave_barrier();
     }
     if (!more) return;
@@ -768,22 +773,23 @@ hipError_t launch_tile(const MmLaunch& a, hipStream_t st) {
   static const hipError_t set =
       hipFuncSetAttribute(reinterpret_cast<const void*>(k), hipFuncAttributeMaxDynamicSharedMemorySize, G::Lds);
   if (set != hipSuccess) return set;
-  const int64_t tiles = row_tiles * col_tiles;
-  k<<<dim3((uint32_t)(tiles < kCUs ? tiles : kCUs)), G::Threads, G::Lds, st>>>(a, (int)col_tiles);
+  const int64_t tiles = row_tiles * col_tiles, most = kCUs * (2 * G::Lds <= 160 * 1024 ? 2 : 1);
+  k<<<dim3((uint32_t)(tiles < most ? tiles : most)), G::Threads, G::Lds, st>>>(a, (int)col_tiles);
   return hipGetLastError();
 }
 
-// Waves of 32 MI x 32 NI results, WN of them across; the exact product's need the registers
-// of a wave that has a SIMD for itself in the large tile (ENI, EWN).
-template <int MI, int NI, int WN, int ENI, int EWN, int KS, int R>
+// Waves of 32 MI x 32 NI results, WN of them across, KS groups; the exact product's need the
+// registers of a wave that has a SIMD for itself in the large tile (ENI, EWN), and those with
+// FP8 rows of A that are not exact take KS8 groups.
+template <int MI, int NI, int WN, int ENI, int EWN, int KS, int KS8, int R>
 hipError_t launch_sized(const MmLaunch& a, hipStream_t st) {
   const bool f32 = a.ep.out_f32;
   if (a.a_fmt && a.b_fmt)
     return f32 ? launch_tile<true, true, true, MI, ENI, EWN, KS, R, false, false, float>(a, st)
-               : launch_tile<true, true, false, MI, NI, WN, KS, R, false, false, __bf16>(a, st);
+               : launch_tile<true, true, false, MI, NI, WN, KS8, R, false, false, __bf16>(a, st);
   if (a.a_fmt)
     return f32 ? launch_tile<true, false, true, MI, ENI, EWN, KS, R, false, false, float>(a, st)
-               : launch_tile<true, false, false, MI, NI, WN, KS, R, false, false, __bf16>(a, st);
+               : launch_tile<true, false, false, MI, NI, WN, KS8, R, false, false, __bf16>(a, st);
   if (a.k % 128)
     return f32 ? launch_tile<false, false, false, MI, NI, WN, KS, R, true, false, float>(a, st)
                : launch_tile<false, false, false, MI, NI, WN, KS, R, true, false, __bf16>(a, st);
@@ -793,24 +799,33 @@ hipError_t launch_sized(const MmLaunch& a, hipStream_t st) {
 
 }  // namespace
 
-hipError_t launch_gemm_tiles(const MmLaunch& a, bool large, hipStream_t st) {
-  return large ? launch_sized<4, 2, 4, 4, 2, 1, 2>(a, st) : launch_sized<2, 2, 2, 2, 2, 2, 4>(a, st);
+hipError_t launch_gemm_tiles(const MmLaunch& a, int side, hipStream_t st) {
+  if (side == 256) return launch_sized<4, 2, 4, 4, 2, 1, 1, 2>(a, st);
+  return side == 128 ? launch_sized<2, 2, 2, 2, 2, 2, 1, 4>(a, st) : launch_sized<1, 1, 2, 1, 2, 1, 1, 4>(a, st);
 }
 
-bool large_tiles(int64_t rows, int64_t cols, int64_t extra_rows, int64_t each) {
-  auto rounds = [&](int64_t side) {
+int tile_side(int64_t rows, int64_t cols, int64_t extra_rows, int64_t each) {
+  auto rounds = [&](int64_t side, int64_t at_once) {
     const int64_t tiles = (rows / side + extra_rows + 1) * ((cols + side - 1) / side) * each;
-    return (tiles + kCUs - 1) / kCUs;
+    return (tiles + at_once - 1) / at_once;
   };
-  return 22 * rounds(256) <= 10 * rounds(128);
+  if (rounds(64, 2 * kCUs) == 1) return 64;
+  return 22 * rounds(256, kCUs) <= 10 * rounds(128, kCUs) ? 256 : 128;
 }
 
 hipError_t launch_grouped_wgrad(const MmLaunch& a, hipStream_t st) {
-  if (large_tiles(a.n - 1, a.k, 0, a.groups))
-    return a.ep.out_f32 ? launch_tile<true, true, true, 4, 4, 2, 1, 2, false, true, float>(a, st)
-                        : launch_tile<true, true, false, 4, 2, 4, 1, 2, false, true, __bf16>(a, st);
-  return a.ep.out_f32 ? launch_tile<true, true, true, 2, 2, 2, 2, 4, false, true, float>(a, st)
-                      : launch_tile<true, true, false, 2, 2, 2, 2, 4, false, true, __bf16>(a, st);
+  const bool f32 = a.ep.out_f32;
+  switch (tile_side(a.n - 1, a.k, 0, a.groups)) {
+    case 64:
+      return f32 ? launch_tile<true, true, true, 1, 1, 2, 1, 4, false, true, float>(a, st)
+                 : launch_tile<true, true, false, 1, 1, 2, 1, 4, false, true, __bf16>(a, st);
+    case 128:
+      return f32 ? launch_tile<true, true, true, 2, 2, 2, 2, 4, false, true, float>(a, st)
+                 : launch_tile<true, true, false, 2, 2, 2, 1, 4, false, true, __bf16>(a, st);
+    default:
+      return f32 ? launch_tile<true, true, true, 4, 4, 2, 1, 2, false, true, float>(a, st)
+                 : launch_tile<true, true, false, 4, 2, 4, 1, 2, false, true, __bf16>(a, st);
+  }
 }
 
 }  // namespace mxq
