@@ -13,7 +13,7 @@ namespace {
 constexpr int64_t kMaxDim = ((int64_t)1 << 31) - 1;  // rows and columns
 constexpr int64_t kMaxK = (int64_t)1 << 22;          // tile-relative byte offsets stay within 32 bits
 constexpr int64_t kMaxLd = (int64_t)1 << 23;         // the same for columns of tokens
-constexpr int64_t kMaxGrid = (int64_t)1 << 30;       // workgroups of one launch, at the smallest tile
+constexpr int64_t kMaxGrid = (int64_t)1 << 30;       // results in tiles of 32 x 32: tiles are counted in 32 bits
 
 bool aligned(const void* p, uintptr_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
 
@@ -136,7 +136,8 @@ mxq_status mxq_act_grad(const void* dy, const void* z, mxq_dtype dt, int64_t row
   if (n == 0 || n > kMaxDim || rows > kMaxDim || rows > ((int64_t)1 << 40) / n) return MXQ_ESHAPE;
   if (act == MXQ_ACT_SWIGLU && n % 2) return MXQ_ESHAPE;
   // the grids enumerate row blocks x column tiles and groups x column tiles
-  if (act_grad_blocks(rows, n_experts, act_grad_rows(rows, n)) * ((n + 511) / 512) >= kMaxGrid / 64 || n_experts * ((n + 63) / 64) >= kMaxGrid / 256)
+  if (act_grad_blocks(rows, n_experts, act_grad_rows(rows, n)) * ((n + 511) / 512) >= kMaxGrid / 64 ||
+      n_experts * ((n + 63) / 64) >= kMaxGrid / 256)
     return MXQ_ESHAPE;
   if (!aligned(dy, 16) || !aligned(z, 16) || !aligned(dz, 16) || !aligned(db, 16) || !aligned(workspace, 16) ||
       !aligned(offsets, 8))

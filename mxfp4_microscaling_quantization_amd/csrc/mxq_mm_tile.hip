@@ -55,12 +55,14 @@ __device__ __forceinline__ v4i buffer_of(const void* base, int64_t bytes) {
 // precedes their first reader. (Written in assembly because the compiler would wait
 // for all of them ahead of every LDS read.)
 __device__ __forceinline__ void load_lds16(v4i buf, uint32_t voff, uint32_t soff, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds" ::"s"(__builtin_amdgcn_readfirstlane(lds)),
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds" ::"s"(
+                   __builtin_amdgcn_readfirstlane(lds)),
                "v"(voff), "s"(buf), "s"(__builtin_amdgcn_readfirstlane(soff))
                : "memory");
 }
 __device__ __forceinline__ void load_lds4(v4i buf, uint32_t voff, uint32_t soff, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, %3 offen lds" ::"s"(__builtin_amdgcn_readfirstlane(lds)),
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, %3 offen lds" ::"s"(
+                   __builtin_amdgcn_readfirstlane(lds)),
                "v"(voff), "s"(buf), "s"(__builtin_amdgcn_readfirstlane(soff))
                : "memory");
 }
