@@ -35,13 +35,13 @@ struct MmLaunch {
 hipError_t launch_gemm_rows(const MmLaunch& a, bool few, hipStream_t st);
 // The tiled kernel: `side` x `side` results of a workgroup (64, 128 or 256).
 hipError_t launch_gemm_tiles(const MmLaunch& a, int side, hipStream_t st);
-// The side for `each` results of rows x cols (extra_rows: started row tiles beyond those). Tiles of
-// 64 while all of them run at once, two on each of the 256 CUs (MXFP4 / FP8, k 4096, 64 and 128, us:
+// The side for `each` results of rows x cols, the rows those of `experts` (0: of one matrix), each of
+// which has a row tile at least and half of one over on average. Tiles of 64 while all of them run at once, two on each of the 256 CUs (MXFP4 / FP8, k 4096, 64 and 128, us:
 // 256 x 4096 results 11.0 and 15.1 / 12.8 and 20.4, 512 x 4096 13.8 and 15.8 / 18.1 and 21.8,
 // 256 x 14336 25.7 and 17.6 / 33.8 and 24.0). A tile of 256 takes about 2.2 times one of 128's time
 // for four times its results, and 256 of either run at once (MXFP4, k 4096, 256 and 128, us:
 // 1024 x 4096 results 32.0 and 17.9, 2048 x 4096 33.3 and 31.5, 4096 x 4096 40.0 and 58.2).
-int tile_side(int64_t rows, int64_t cols, int64_t extra_rows, int64_t each);
+int tile_side(int64_t rows, int64_t cols, int64_t experts, int64_t each);
 hipError_t launch_gemm(const MmLaunch& a, hipStream_t st);
 
 // The weight gradient of every expert: a = dY's FP8 columns [n, ld_a], b = X's [k, ld_b],

@@ -814,9 +814,11 @@ hipError_t launch_gemm_tiles(const MmLaunch& a, int side, hipStream_t st) {
   return side == 128 ? launch_sized<2, 2, 2, 2, 2, 2, 1, 4>(a, st) : launch_sized<1, 1, 2, 1, 2, 1, 1, 4>(a, st);
 }
 
-int tile_side(int64_t rows, int64_t cols, int64_t extra_rows, int64_t each) {
+int tile_side(int64_t rows, int64_t cols, int64_t experts, int64_t each) {
+  const int64_t least = rows < experts ? rows : experts;
   auto rounds = [&](int64_t side, int64_t at_once) {
-    const int64_t tiles = (rows / side + extra_rows + 1) * ((cols + side - 1) / side) * each;
+    const int64_t full = rows / side + experts / 2 + 1;
+    const int64_t tiles = (full < least ? least : full) * ((cols + side - 1) / side) * each;
     return (tiles + at_once - 1) / at_once;
   };
   if (rounds(64, 2 * kCUs) == 1) return 64;
