@@ -142,14 +142,8 @@ __global__ __launch_bounds__(64 * kLanes) void act_grad_sum_kernel(ActGradLaunch
   const int64_t col = (int64_t)(blockIdx.x % col_tiles) * 64 + lane;
   const int each = p.block_rows;
   int first = 0, blocks = (int)((p.rows + each - 1) / each);
-  if (p.offsets) {
-    first = segment_tiles(p.offsets, g, p.rows, each);
-    const int64_t c = clamp_row(p.offsets[g + 1], p.rows) - clamp_row(p.offsets[g], p.rows);
-    blocks = c > 0 ? (int)((c + each - 1) / each) : 0;
-    // malformed offsets stay inside the workspace
-    const int most = (int)act_grad_blocks(p.rows, p.groups, each);
-    blocks = first >= most ? 0 : first + blocks > most ? most - first : blocks;
-  }
+  // (malformed offsets stay inside the workspace)
+  if (p.offsets) blocks = tiles_of(p.offsets, g, p.rows, each, (int)act_grad_blocks(p.rows, p.groups, each), first);
   float sum = 0.0f;
   if (col < p.n) {
     const float* q = p.partials + (int64_t)first * p.n + col;

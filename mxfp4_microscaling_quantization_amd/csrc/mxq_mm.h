@@ -1,9 +1,10 @@
 // Device-side building blocks of the matrix products: fragments of the 32x32 matrix
-// instructions, the epilogue, and the walk over experts' token segments.
+// instructions and the epilogue.
 #pragma once
 
 #include "mxq_device.h"
 #include "mxq_mm_launch.h"
+#include "mxq_mm_segments.h"
 
 namespace mxq {
 
@@ -281,67 +282,5 @@ struct RunEpilogue {
     }
   }
 };
-
-// ---------------------------------------------------------------------------
-// Token segments. Expert e owns rows [offsets[e], offsets[e + 1]), clamped to [0, rows].
-struct Segment {
-  int expert;
-  int64_t begin;  // first row of the expert
-  int64_t count;  // its rows
-  int tile;       // which of the expert's tiles
-};
-
-__device__ __forceinline__ int64_t clamp_row(int64_t v, int64_t rows) {
-  return v < 0 ? 0 : v > rows ? rows : v;
-}
-
-// Tiles of `step` rows over all segments, in expert order: their number.
-__device__ __forceinline__ int segment_tiles(const int64_t* offsets, int experts, int64_t rows, int step) {
-  const int lane = threadIdx.x & 63;
-  int sum = 0;
-  for (int e = lane; e < experts; e += 64) {
-    const int64_t c = clamp_row(offsets[e + 1], rows) - clamp_row(offsets[e], rows);
-    sum += c > 0 ? (int)((c + step - 1) / step) : 0;
-  }
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) sum += __shfl_xor(sum, d);
-  return __builtin_amdgcn_readfirstlane(sum);
-}
-
-// The segment that holds tile `index`; false past the last one. Every wave of a
-// workgroup finds it for itself: 64 experts a turn, an inclusive scan over the lanes.
-__device__ __forceinline__ bool find_segment(const int64_t* offsets, int experts, int64_t rows, int step, int index,
-                                             Segment& s) {
-  const int lane = threadIdx.x & 63;
-  int before = 0;
-  for (int e0 = 0; e0 < experts; e0 += 64) {
-    const int e = e0 + lane;
-    int64_t begin = 0, count = 0;
-    if (e < experts) {
-      begin = clamp_row(offsets[e], rows);
-      count = clamp_row(offsets[e + 1], rows) - begin;
-      if (count < 0) count = 0;
-    }
-    const int tiles = (int)((count + step - 1) / step);
-    int inc = tiles;
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-      const int up = __shfl_up(inc, d);
-      if (lane >= d) inc += up;
-    }
-    const unsigned long long past = __ballot(inc > index - before);
-    if (past) {
-      const int at = __builtin_ctzll(past);
-      s.expert = e0 + at;
-      // rows < 2^31
-      s.begin = (uint32_t)__builtin_amdgcn_readlane((int)begin, at);
-      s.count = (uint32_t)__builtin_amdgcn_readlane((int)count, at);
-      s.tile = index - before - __builtin_amdgcn_readlane(inc - tiles, at);
-      return true;
-    }
-    before += __builtin_amdgcn_readlane(inc, 63);
-  }
-  return false;
-}
 
 }  // namespace mxq

@@ -176,8 +176,7 @@ __global__ __launch_bounds__(64 * W, 1) void mm_rows_kernel(MmLaunch p, int col_
 template <bool A8, bool B8, int MT, int NT, int W, int D>
 hipError_t launch_waves(const MmLaunch& a, hipStream_t st) {
   const int64_t col_tiles = (a.n + 16 * NT - 1) / (16 * NT);
-  const int64_t row_tiles = a.offsets ? a.rows / (16 * MT) + (a.rows < a.groups ? a.rows : a.groups)
-                                      : (a.rows + 16 * MT - 1) / (16 * MT);
+  const int64_t row_tiles = a.offsets ? most_tiles(a.rows, a.groups, 16 * MT) : (a.rows + 16 * MT - 1) / (16 * MT);
   const dim3 grid((uint32_t)(row_tiles * col_tiles));
   if (a.ep.out_f32)
     mm_rows_kernel<A8, B8, MT, NT, W, D, float><<<grid, 64 * W, 0, st>>>(a, (int)col_tiles);

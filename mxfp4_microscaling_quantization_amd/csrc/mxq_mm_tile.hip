@@ -200,8 +200,13 @@ __global__ __launch_bounds__(128 * WN * KS, MI * NI > 8 ? 1 : 2) void mm_tile_ke
   const int r = lane & 31, h = lane >> 5;
 
   const bool listed = p.offsets && !WG;  // its row tiles are known on the device only
-  const int row_tiles = listed ? segment_tiles(p.offsets, p.groups, p.rows, G::BM)
-                               : (int)(((WG ? p.n : p.rows) + G::BM - 1) / G::BM);
+  int row_tiles = (int)(((WG ? p.n : p.rows) + G::BM - 1) / G::BM);
+  if (listed) {
+    // (malformed offsets make no more work than well-formed ones can)
+    const int most = (int)most_tiles(p.rows, p.groups, G::BM);
+    row_tiles = segment_tiles(p.offsets, p.groups, p.rows, G::BM);
+    row_tiles = row_tiles < most ? row_tiles : most;
+  }
   const int64_t total = (int64_t)row_tiles * col_tiles * (WG ? p.groups : 1);
   const int64_t abytes = WG ? p.ld_a : A8 ? p.k : p.k / 2, bbytes = WG ? p.ld_b : B8 ? p.k : p.k / 2;
   const int64_t asbytes = WG ? 4 * p.ld_as : A8 ? p.k / 128 * 4 : p.k / 32;
@@ -777,7 +782,7 @@ hipError_t launch_tile(const MmLaunch& a, hipStream_t st) {
   using G = Tile<A8, B8, MI, NI, WN, KS, R, WG>;
   const int64_t col_tiles = ((WG ? a.k : a.n) + G::BN - 1) / G::BN;
   const int64_t row_tiles = WG          ? (a.n + G::BM - 1) / G::BM * a.groups
-                            : a.offsets ? a.rows / G::BM + (a.rows < a.groups ? a.rows : a.groups)
+                            : a.offsets ? most_tiles(a.rows, a.groups, G::BM)
                                         : (a.rows + G::BM - 1) / G::BM;
   auto k = mm_tile_kernel<A8, B8, EXACT, MI, NI, WN, KS, R, ODDK, WG, T>;
   static const hipError_t set =
