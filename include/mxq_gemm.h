@@ -61,7 +61,7 @@ typedef enum {
  * z            [m, n] of d_dt, or NULL: z as mxq_act_grad takes it. It must not
  *              overlap d or residual.
  * Alignment: codes 16 bytes, fp32 scales and fp32 bias 4, bf16 bias 2, residual, d and
- * z 16. m >= 0 (0: nothing is done), 1 <= n < 2^31, m < 2^31, 1 <= k <= 2^22.
+ * z 16; E8M0 scales may start at any byte (on a multiple of 4 they are read faster). m >= 0 (0: nothing is done), 1 <= n < 2^31, m < 2^31, 1 <= k <= 2^22.
  */
 mxq_status mxq_gemm(const uint8_t* a, const void* a_scales, mxq_operand a_fmt, const uint8_t* b,
                     const void* b_scales, mxq_operand b_fmt, int64_t m, int64_t n, int64_t k,

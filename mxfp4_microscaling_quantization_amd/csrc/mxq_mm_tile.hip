@@ -192,7 +192,7 @@ __device__ __forceinline__ int64_t list_entry(int64_t turn) {
   return turn * grid + x * q + (x < r ? x : r) + (blockIdx.x >> 3);
 }
 
-template <bool A8, bool B8, bool EXACT, int MI, int NI, int WN, int KS, int R, bool ODDK, bool WG, typename T>
+template <bool A8, bool B8, bool EXACT, int MI, int NI, int WN, int KS, int R, bool LOOSE, bool WG, typename T>
 __global__ __launch_bounds__(128 * WN * KS, MI * NI > 8 ? 1 : 2) void mm_tile_kernel(MmLaunch p, int col_tiles) {
   using G = Tile<A8, B8, MI, NI, WN, KS, R, WG>;
   extern __shared__ __align__(16) uint8_t lds[];
@@ -423,7 +423,8 @@ __global__ __launch_bounds__(128 * WN * KS, MI * NI > 8 ? 1 : 2) void mm_tile_ke
                   slot + first * 16);
     }
   };
-  // The same through registers where rows of block bytes do not start on dwords.
+  // The same through registers (LOOSE) where rows of block bytes do not start on dwords: k is not a
+  // multiple of 128, or the caller's scales start at another byte.
   constexpr int SR = (G::SRows + G::Threads - 1) / G::Threads;
   v4i held[SR];
   auto fetch_scales = [&](int c) {
@@ -535,7 +536,7 @@ __global__ __launch_bounds__(128 * WN * KS, MI * NI > 8 ? 1 : 2) void mm_tile_ke
   // last one only what the steps to come do not load.
   auto start_first = [&]() {
     if (WG && turns == 0) return;
-    if constexpr (ODDK) {
+    if constexpr (LOOSE) {
       fetch_scales(0);
       park_scales(0);
     } else {
@@ -591,7 +592,7 @@ __global__ __launch_bounds__(128 * WN * KS, MI * NI > 8 ? 1 : 2) void mm_tile_ke
     if (!WG || turns > 0) {
       wait_loads<KS == 2 && A8 ? G::DA + G::DB : PartA + PartB + (R - 2) * (G::DA + G::DB)>();
       barrier();
-      if (ODDK && (tail & 1) && turns == 1) clear_tail();
+      if (LOOSE && (tail & 1) && turns == 1) clear_tail();
       if (WG && (KS == 2 ? turns == 1 : halves == 1)) clear_group(halves - 1);
       read_step(0, 0);
       if constexpr (Roll) {
@@ -605,7 +606,7 @@ __global__ __launch_bounds__(128 * WN * KS, MI * NI > 8 ? 1 : 2) void mm_tile_ke
         for (int t = 0; t + 1 < turns; ++t) {
           asm volatile("" : "+v"(abase), "+v"(bbase));
           if constexpr (WG) asm volatile("" : "+v"(keep_second));
-          if constexpr (ODDK) {
+          if constexpr (LOOSE) {
             if ((t & 1) == 0 && t + 2 < turns) fetch_scales((t >> 1) + 1);
             if ((t & 1) == 1) park_scales((t >> 1) + 1);
           }
@@ -618,9 +619,9 @@ __global__ __launch_bounds__(128 * WN * KS, MI * NI > 8 ? 1 : 2) void mm_tile_ke
           wait_loads<G::Younger>();
           barrier();
           if (WG && t + 2 == turns) clear_group(halves - 1);
-          if (ODDK && (tail & 1) && t + 2 == turns) clear_tail();
+          if (LOOSE && (tail & 1) && t + 2 == turns) clear_tail();
           trim(t + R);
-          if constexpr (!ODDK)
+          if constexpr (!LOOSE)
             if ((t & 1) == 0 && t + 2 * G::Ahead < turns) load_scales((t >> 1) + G::Ahead);
           read_step(t + 1, 0);
           read_scales(2 * t + 2 + kg);
@@ -645,7 +646,7 @@ __global__ __launch_bounds__(128 * WN * KS, MI * NI > 8 ? 1 : 2) void mm_tile_ke
           // addresses and masks are formed where used, not held
           asm volatile("" : "+v"(abase), "+v"(bbase));
           if constexpr (WG) asm volatile("" : "+v"(keep_second));
-          if constexpr (ODDK) {
+          if constexpr (LOOSE) {
             // chunk c + 1 is fetched in the first turn of chunk c and parked in the second
             if ((t & 1) == 0 && t + 2 < turns) fetch_scales((t >> 1) + 1);
             if ((t & 1) == 1 && t + 1 < turns) park_scales((t >> 1) + 1);
@@ -661,9 +662,9 @@ __global__ __launch_bounds__(128 * WN * KS, MI * NI > 8 ? 1 : 2) void mm_tile_ke
                 if (WG && s == 3 && t + 2 == turns && (halves & 1)) clear_group(halves - 1);
               }
               if (s == 3) {
-                if (ODDK && (tail & 1) && t + 2 == turns) clear_tail();
+                if (LOOSE && (tail & 1) && t + 2 == turns) clear_tail();
                 trim(t + R);
-                if constexpr (!ODDK)
+                if constexpr (!LOOSE)
                   if ((t & 1) == 0 && t + 2 * G::Ahead < turns) load_scales((t >> 1) + G::Ahead);
               }
               read_step(tn, sn);
@@ -688,7 +689,7 @@ __global__ __launch_bounds__(128 * WN * KS, MI * NI > 8 ? 1 : 2) void mm_tile_ke
           }
         }
         last_step(0);
-        if (!ODDK || last_steps > 1) {
+        if (!LOOSE || last_steps > 1) {
           if constexpr (A8 || B8) {
             wait_loads<G::Younger>();
             barrier();
@@ -697,7 +698,7 @@ __global__ __launch_bounds__(128 * WN * KS, MI * NI > 8 ? 1 : 2) void mm_tile_ke
           last_step(1);
           if (last_steps > 2) {
             last_step(2);
-            if (!ODDK || last_steps > 3) last_step(3);
+            if (!LOOSE || last_steps > 3) last_step(3);
           }
         }
       }
@@ -777,14 +778,14 @@ __global__ __launch_bounds__(128 * WN * KS, MI * NI > 8 ? 1 : 2) void mm_tile_ke
   }
 }
 
-template <bool A8, bool B8, bool EXACT, int MI, int NI, int WN, int KS, int R, bool ODDK, bool WG, typename T>
+template <bool A8, bool B8, bool EXACT, int MI, int NI, int WN, int KS, int R, bool LOOSE, bool WG, typename T>
 hipError_t launch_tile(const MmLaunch& a, hipStream_t st) {
   using G = Tile<A8, B8, MI, NI, WN, KS, R, WG>;
   const int64_t col_tiles = ((WG ? a.k : a.n) + G::BN - 1) / G::BN;
   const int64_t row_tiles = WG          ? (a.n + G::BM - 1) / G::BM * a.groups
                             : a.offsets ? most_tiles(a.rows, a.groups, G::BM)
                                         : (a.rows + G::BM - 1) / G::BM;
-  auto k = mm_tile_kernel<A8, B8, EXACT, MI, NI, WN, KS, R, ODDK, WG, T>;
+  auto k = mm_tile_kernel<A8, B8, EXACT, MI, NI, WN, KS, R, LOOSE, WG, T>;
   static const hipError_t set =
       hipFuncSetAttribute(reinterpret_cast<const void*>(k), hipFuncAttributeMaxDynamicSharedMemorySize, G::Lds);
   if (set != hipSuccess) return set;
@@ -802,10 +803,14 @@ hipError_t launch_sized(const MmLaunch& a, hipStream_t st) {
   if (a.a_fmt && a.b_fmt)
     return f32 ? launch_tile<true, true, true, MI, ENI, EWN, KS, R, false, false, float>(a, st)
                : launch_tile<true, true, false, MI, NI, WN, KS8, R, false, false, __bf16>(a, st);
+  const bool loose = a.k % 128 || ((uintptr_t)a.a_scales | (uintptr_t)a.b_scales) % 4;
+  if (a.a_fmt && loose)
+    return f32 ? launch_tile<true, false, true, MI, ENI, EWN, KS, R, true, false, float>(a, st)
+               : launch_tile<true, false, false, MI, NI, WN, KS8, R, true, false, __bf16>(a, st);
   if (a.a_fmt)
     return f32 ? launch_tile<true, false, true, MI, ENI, EWN, KS, R, false, false, float>(a, st)
                : launch_tile<true, false, false, MI, NI, WN, KS8, R, false, false, __bf16>(a, st);
-  if (a.k % 128)
+  if (loose)
     return f32 ? launch_tile<false, false, false, MI, NI, WN, KS, R, true, false, float>(a, st)
                : launch_tile<false, false, false, MI, NI, WN, KS, R, true, false, __bf16>(a, st);
   return f32 ? launch_tile<false, false, false, MI, NI, WN, KS, R, false, false, float>(a, st)

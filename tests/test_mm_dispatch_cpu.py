@@ -1,0 +1,40 @@
+"""Which kernel a call of the products takes, without a GPU (tests/hip_recorder.py)."""
+import pytest
+
+from tests.hip_recorder import record
+
+BASE = 0x10000  # a 16-byte aligned, never dereferenced address
+
+
+def gemm(m, n, k, fmt="44", fp32=False, a_scales=BASE, b_scales=BASE, device=0, failures=0):
+    return (device, failures, "mxq_gemm", [BASE, a_scales, int(fmt[0] == "8"), BASE, b_scales, int(fmt[1] == "8"), m, n,
+                                           k, None, 1, 0, None, BASE, int(fp32), None, None])
+
+
+def grouped(rows, n, k, experts, fmt="44", fp32=False, a_scales=BASE, b_scales=BASE):
+    return (0, 0, "mxq_grouped_gemm", [BASE, a_scales, int(fmt[0] == "8"), BASE, b_scales, int(fmt[1] == "8"), rows, n,
+                                       k, BASE, experts, None, 1, 0, None, BASE, int(fp32), None, None])
+
+
+# template arguments of mm_tile_kernel: FP8 A, FP8 B, exact, 32-row and 32-column blocks of a
+# wave, waves across, wave groups, ring slots, scales through registers, weight gradient, result
+LOOSE = 8
+
+
+@pytest.mark.parametrize("fmt", ["44", "84"])
+@pytest.mark.parametrize("fp32", [False, True])
+def test_scales_that_start_off_a_dword_take_no_dword_loads(fmt, fp32, tmp_path):
+    shapes = [(130, 1100, 512), (700, 4200, 512), (4130, 4100, 512)]
+    offsets = [(a, b) for a in range(4) for b in range(4) if fmt[0] == "4" or a == 0]
+    calls = [make(*s, fmt=fmt, fp32=fp32, a_scales=BASE + a, b_scales=BASE + b)
+             for make in (gemm, lambda m, n, k, **kw: grouped(m, n, k, 3, **kw)) for s in shapes for a, b in offsets]
+    got = record(calls, tmp_path)
+    sides = set()
+    for call, (status, launches, _) in zip(calls, got):
+        assert status == 0 and len(launches) == 1
+        name, args = launches[0][1]
+        assert name == "mm_tile_kernel"
+        sides.add(args[3:8])
+        args_of = call[3]
+        assert args[LOOSE] == bool((args_of[1] | args_of[4]) % 4), call
+    assert len(sides) == 3
