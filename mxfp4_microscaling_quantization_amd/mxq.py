@@ -309,6 +309,16 @@ def _offsets(offsets: torch.Tensor) -> int:
     return offsets.numel() - 1
 
 
+def _on_gpu(*tensors: Optional[torch.Tensor]) -> int:
+    """The current stream of the current GPU, on which all of these tensors must be: a kernel
+    that follows a host pointer, or another GPU's, ends the process."""
+    where = {t.get_device() for t in tensors if t is not None}  # -1: host memory
+    if min(where) < 0 or where != {torch._C._cuda_getDevice()}:
+        raise ValueError("tensors on the current GPU expected, got some on "
+                         f"{sorted({str(t.device) for t in tensors if t is not None})}")
+    return _stream()
+
+
 def _product(a, b, offsets, bias, act, residual, preact, out_dtype, out):
     ap, asp, afmt, k, ashape = _operand(a, 2)
     bp, bsp, bfmt, bk, bshape = _operand(b, 2 if offsets is None else 3)
@@ -333,15 +343,16 @@ def _product(a, b, offsets, bias, act, residual, preact, out_dtype, out):
     if bias is not None:
         bdt = _float_code(bias.dtype)
         bias_p = _dense(bias, bshape[:-1], bias.dtype, "bias")
+    stream = _on_gpu(*a, *b, d, offsets, bias, residual, z)
     if offsets is None:
         status = lib().mxq_gemm(ap, asp, afmt, bp, bsp, bfmt, m, n, k, bias_p, bdt, code, rp, d.data_ptr(), dt, zp,
-                                _stream())
+                                stream)
     else:
         experts = _offsets(offsets)
         if bshape[0] != experts:
             raise ValueError(f"{bshape[0]} weights for {experts} experts")
         status = lib().mxq_grouped_gemm(ap, asp, afmt, bp, bsp, bfmt, m, n, k, offsets.data_ptr(), experts, bias_p,
-                                        bdt, code, rp, d.data_ptr(), dt, zp, _stream())
+                                        bdt, code, rp, d.data_ptr(), dt, zp, stream)
     _check(status)
     return (d, z) if preact else d
 
@@ -387,9 +398,10 @@ def mxq_grouped_wgrad(y, x, offsets: torch.Tensor, rows: int, add: Optional[torc
         d, out_dtype = out, out.dtype
     dt, dp = _float_code(out_dtype), _dense(d, shape, out_dtype, "out")
     addp = None if add is None else _dense(add, shape, out_dtype, "add")
+    stream = _on_gpu(yq, ys, xq, xs, d, offsets, add)
     _check(lib().mxq_grouped_wgrad(yq.data_ptr(), ys.data_ptr(), yq.stride(0), ys.stride(0), xq.data_ptr(),
                                    xs.data_ptr(), xq.stride(0), xs.stride(0), rows, n, k, offsets.data_ptr(), experts,
-                                   addp, dp, dt, _stream()))
+                                   addp, dp, dt, stream))
     return d
 
 
@@ -419,5 +431,6 @@ def mxq_act_grad(dy: torch.Tensor, z: torch.Tensor, act: str = "none", offsets: 
         elif workspace.numel() * workspace.element_size() < need:
             raise ValueError(f"workspace of {need} bytes expected")
         wsp = workspace.data_ptr()
-    _check(lib().mxq_act_grad(dyp, zp, dt, rows, n, code, offp, groups, dzp, dbp, wsp, _stream()))
+    stream = _on_gpu(dy, z, dz, offsets, *((db, workspace) if bias_grad else ()))
+    _check(lib().mxq_act_grad(dyp, zp, dt, rows, n, code, offp, groups, dzp, dbp, wsp, stream))
     return (dz, db) if bias_grad else dz
