@@ -309,13 +309,17 @@ def _offsets(offsets: torch.Tensor) -> int:
     return offsets.numel() - 1
 
 
-def _on_gpu(*tensors: Optional[torch.Tensor]) -> int:
+def _on_gpu(first: torch.Tensor, *others: Optional[torch.Tensor]) -> int:
     """The current stream of the current GPU, on which all of these tensors must be: a kernel
     that follows a host pointer, or another GPU's, ends the process."""
-    where = {t.get_device() for t in tensors if t is not None}  # -1: host memory
-    if min(where) < 0 or where != {torch._C._cuda_getDevice()}:
-        raise ValueError("tensors on the current GPU expected, got some on "
-                         f"{sorted({str(t.device) for t in tensors if t is not None})}")
+    device = first.get_device()  # -1: host memory
+    elsewhere = device < 0
+    for t in others:
+        if t is not None and t.get_device() != device:
+            elsewhere = True
+    if elsewhere or device != torch._C._cuda_getDevice():
+        where = sorted({str(t.device) for t in (first, *others) if t is not None})
+        raise ValueError(f"tensors on the current GPU expected, got some on {', '.join(where)}")
     return _stream()
 
 
@@ -343,7 +347,8 @@ def _product(a, b, offsets, bias, act, residual, preact, out_dtype, out):
     if bias is not None:
         bdt = _float_code(bias.dtype)
         bias_p = _dense(bias, bshape[:-1], bias.dtype, "bias")
-    stream = _on_gpu(*a, *b, d, offsets, bias, residual, z)
+    given = () if out is None else (d, z)
+    stream = _on_gpu(*a, *b, offsets, bias, residual, *given)
     if offsets is None:
         status = lib().mxq_gemm(ap, asp, afmt, bp, bsp, bfmt, m, n, k, bias_p, bdt, code, rp, d.data_ptr(), dt, zp,
                                 stream)
