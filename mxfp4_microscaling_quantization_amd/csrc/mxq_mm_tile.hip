@@ -58,21 +58,20 @@ __device__ __forceinline__ v4i buffer_of(const void* base, int64_t bytes) {
   return v4i{(int)(uint32_t)a, (int)((a >> 32) & 0xFFFFu), (int)n, 0x00020000};
 }
 
-// Direct loads into LDS: lane l's 16 (or 4) bytes land at lds + 16 l (4 l). They have no
+// Direct loads into LDS: lane l's 16 (or 4) bytes land at lds + 16 l (4 l), lds in m0, an operand
+// like the others, so that the compiler knows what the register holds. They have no
 // destination register; the kernel waits for them by count before the barrier that
 // precedes their first reader. (Written in assembly because the compiler would wait
 // for all of them ahead of every LDS read.) A vector memory instruction may read a scalar
 // register five wait states after a vector instruction wrote it: the compiler, which does
 // not look into the statement, may just have fetched a spilled descriptor with v_readlane.
 __device__ __forceinline__ void load_lds16(v4i buf, uint32_t voff, uint32_t soff, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds" ::"s"(
-                   __builtin_amdgcn_readfirstlane(lds)),
+  asm volatile("s_nop 4\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds" ::"{m0}"(__builtin_amdgcn_readfirstlane(lds)),
                "v"(voff), "s"(buf), "s"(__builtin_amdgcn_readfirstlane(soff))
                : "memory");
 }
 __device__ __forceinline__ void load_lds4(v4i buf, uint32_t voff, uint32_t soff, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dword %1, %2, %3 offen lds" ::"s"(
-                   __builtin_amdgcn_readfirstlane(lds)),
+  asm volatile("s_nop 4\n\tbuffer_load_dword %1, %2, %3 offen lds" ::"{m0}"(__builtin_amdgcn_readfirstlane(lds)),
                "v"(voff), "s"(buf), "s"(__builtin_amdgcn_readfirstlane(soff))
                : "memory");
 }

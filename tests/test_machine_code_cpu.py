@@ -1,7 +1,8 @@
 """The library's own machine code, disassembled: a scalar register that a vector instruction
 writes (a spilled value fetched by v_readlane, say) is read by a vector memory instruction
 five wait states later at the earliest. The compiler sees to that among its own
-instructions, but not for those inside assembly statements."""
+instructions, but not for those inside assembly statements. And in the sources, no assembly
+statement changes m0 behind the compiler's back."""
 import glob
 import os
 import re
@@ -107,3 +108,13 @@ def test_scalar_registers_of_vector_memory_instructions(kernels):
     bad = {k: v for k, v in bad.items() if v}
     assert not bad, "\n".join(f"{k}: {len(v)}, first after {v[0][0]} wait states: {v[0][1]} | {v[0][2]}"
                               for k, v in bad.items())
+
+
+def test_assembly_statements_leave_m0_to_the_compiler():
+    """m0 is reserved, so a statement cannot name it as clobbered: it may only be an operand."""
+    statements = []
+    for path in glob.glob(os.path.join(os.path.dirname(mxq.LIB_PATH), "csrc*", "*")):
+        statements += re.findall(r"\basm\b[^;]*;", open(path).read())
+    loads = [s for s in statements if "buffer_load" in s]
+    assert loads and all('"{m0}"' in s for s in loads)
+    assert not [s for s in statements if re.search(r"\bm0\b", s.replace('"{m0}"', ""))]
