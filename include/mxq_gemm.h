@@ -91,8 +91,8 @@ mxq_status mxq_grouped_gemm(const uint8_t* a, const void* a_scales, mxq_operand 
  * one per 128-token group of an expert.
  * add, d: [n_experts, n, k] of d_dt; add may be NULL (zero) or d itself. An expert
  * without tokens gives add, or zeros; so does rows == 0.
- * offsets as in mxq_grouped_gemm. rows <= ld_y, ld_x <= 2^23, multiples of 16; ld_ys,
- * ld_xs >= (rows + 127 n_experts) / 128. y, x, add, d 16-byte aligned, scales 4,
+ * offsets as in mxq_grouped_gemm. rows <= ld_y, ld_x <= 2^23, multiples of 16;
+ * (rows + 127 n_experts) / 128 <= ld_ys, ld_xs < 2^22. y, x, add, d 16-byte aligned, scales 4,
  * offsets 8. n, k < 2^31.
  */
 mxq_status mxq_grouped_wgrad(const uint8_t* y, const float* y_scales, int64_t ld_y, int64_t ld_ys,

@@ -13,6 +13,7 @@ namespace {
 constexpr int64_t kMaxDim = ((int64_t)1 << 31) - 1;  // rows and columns
 constexpr int64_t kMaxK = (int64_t)1 << 22;          // tile-relative byte offsets stay within 32 bits
 constexpr int64_t kMaxLd = (int64_t)1 << 23;         // the same for columns of tokens
+constexpr int64_t kMaxLdScales = ((int64_t)1 << 22) - 1;  // and for their scales: 256 rows within 2^32 bytes
 constexpr int64_t kMaxGrid = (int64_t)1 << 30;       // results in tiles of 32 x 32: tiles are counted in 32 bits
 
 bool aligned(const void* p, uintptr_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
@@ -98,6 +99,7 @@ mxq_status mxq_grouped_wgrad(const uint8_t* y, const float* y_scales, int64_t ld
   if (n == 0 || k == 0 || n > kMaxDim || k > kMaxDim || rows > kMaxDim) return MXQ_ESHAPE;
   if (n > ((int64_t)1 << 40) / k || n * k > ((int64_t)1 << 40) / n_experts) return MXQ_ESHAPE;
   if (ld_y < rows || ld_x < rows || ld_y > kMaxLd || ld_x > kMaxLd) return MXQ_ESHAPE;
+  if (ld_ys > kMaxLdScales || ld_xs > kMaxLdScales) return MXQ_ESHAPE;
   if (rows > 0 && (ld_ys < rc_group_slots(rows, n_experts) || ld_xs < rc_group_slots(rows, n_experts)))
     return MXQ_ESHAPE;
   if (((n + 31) / 32) * ((k + 31) / 32) >= kMaxGrid / n_experts) return MXQ_ESHAPE;

@@ -1,0 +1,50 @@
+"""The weight gradient with the widest pitch of scales that it takes (2^22 - 1, scales in a
+wide tensor), and beyond, on each tile side: equal bits to dense scales, or a refusal."""
+import numpy as np
+import pytest
+import torch
+
+from mxfp4_microscaling_quantization_amd import mxq
+from tests.gpu_helpers import require_gpu
+from tests.mm_helpers import columns, gpu
+from tests.test_gpu_wgrad import check_wgrad
+
+pytestmark = pytest.mark.gpu
+
+MOST = 2 ** 22 - 1
+
+
+def wide(scales, pitch):
+    """The same scales as the first columns of rows of `pitch`."""
+    rows, slots = scales.shape
+    out = torch.empty(rows * pitch, device=scales.device).as_strided((rows, slots), (pitch, 1))
+    return out.copy_(scales)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("counts,n,k", [([130, 33, 0, 257], 130, 328), ([300, 47], 700, 4200),
+                                        ([130, 33, 0, 257], 700, 4200)])
+def test_widest_pitch(counts, n, k, dtype):
+    require_gpu()
+    rng = np.random.default_rng(n + len(counts))
+    y, x = columns(rng, n, counts), columns(rng, k, counts)
+    want = check_wgrad(0, counts, n, k, dtype, y=y, x=x)
+    gy, gx = gpu(*y), gpu(*x)
+    off = torch.tensor([0, *np.cumsum(counts)], device="cuda:0")
+    d = mxq.mxq_grouped_wgrad((gy[0], wide(gy[1], MOST)), gx, off, sum(counts), out_dtype=dtype)
+    assert torch.equal(d, want)
+    # (the matrix that the tile's columns come from: a few of its rows, the others are not multiplied)
+    d = mxq.mxq_grouped_wgrad((gy[0][:96], gy[1][:96]), (gx[0][:320], wide(gx[1][:320], MOST)), off, sum(counts),
+                              out_dtype=torch.float32)
+    assert torch.equal(d, mxq.mxq_grouped_wgrad((gy[0][:96], gy[1][:96]), (gx[0][:320], gx[1][:320]), off, sum(counts),
+                                                out_dtype=torch.float32))
+
+
+def test_beyond():
+    require_gpu()
+    rng = np.random.default_rng(0)
+    (yq, ys), x = gpu(*columns(rng, 2, [100])), gpu(*columns(rng, 8, [100]))
+    off = torch.tensor([0, 100], device="cuda:0")
+    for a, b in (((yq, wide(ys, MOST + 1)), x), (x, (yq, wide(ys, 2 ** 23)))):
+        with pytest.raises(mxq.MxqError):
+            mxq.mxq_grouped_wgrad(a, b, off, 100)

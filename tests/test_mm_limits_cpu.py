@@ -1,0 +1,24 @@
+"""Limits of the products' C ABI that keep offsets inside a tile within 32 bits, and the
+activation gradient's workspace, without a GPU."""
+import pytest
+
+from mxfp4_microscaling_quantization_amd import mxq
+from tests.hip_recorder import record
+
+BASE = 0x10000  # a 16-byte aligned, never dereferenced address
+
+
+def wgrad(ld_ys, ld_xs, rows=300):
+    return (0, 0, "mxq_grouped_wgrad", [BASE, BASE, 304, ld_ys, BASE, BASE, 304, ld_xs, rows, 8, 16, BASE, 4, None, BASE,
+                                        0, None])
+
+
+def test_scale_pitch_of_the_weight_gradient(tmp_path):
+    """256 rows of a tile times 4 bytes times the pitch stay below 2^32."""
+    most = 2 ** 22 - 1
+    assert (255 * most + most - 1) * 4 + 4 <= 2 ** 32 < (256 * (most + 1)) * 4 + 1
+    cases = [((most, most), mxq.MXQ_OK), ((most + 1, 10), mxq.MXQ_ESHAPE), ((10, most + 1), mxq.MXQ_ESHAPE),
+             ((2 ** 40, 2 ** 40), mxq.MXQ_ESHAPE)]
+    cases += [((a, b, 0), s) for (a, b), s in cases]
+    got = record([wgrad(*c) for c, _ in cases], tmp_path)
+    assert [(status, len(launches)) for status, launches, _ in got] == [(s, int(s == mxq.MXQ_OK)) for _, s in cases]
