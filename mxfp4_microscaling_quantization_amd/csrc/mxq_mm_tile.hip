@@ -1,5 +1,7 @@
 // Matrix products on MXFP4 / FP8 operands for many rows: LDS-tiled, operands fetched
 // by direct loads into LDS several stages ahead of the matrix instructions.
+#include <atomic>
+
 #include "mxq_mm.h"
 
 namespace mxq {
@@ -779,6 +781,21 @@ __global__ __launch_bounds__(128 * WN * KS, MI * NI > 8 ? 1 : 2) void mm_tile_ke
   }
 }
 
+// The limit of a kernel's dynamic LDS belongs to the kernel on one device: raised at its first
+// launch there (and again after a failure).
+hipError_t allow_lds(const void* kernel, int bytes, std::atomic<uint64_t>& set) {
+  int device = 0;
+  if (const hipError_t e = hipGetDevice(&device); e != hipSuccess) return e;
+  const uint64_t bit = device < 64 ? (uint64_t)1 << device : 0;
+  if (set.load(std::memory_order_relaxed) & bit) return hipSuccess;
+  const hipError_t e = hipFuncSetAttribute(kernel, hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == hipSuccess)
+    set.fetch_or(bit, std::memory_order_relaxed);
+  else
+    (void)hipGetLastError();  // it is returned here
+  return e;
+}
+
 template <bool A8, bool B8, bool EXACT, int MI, int NI, int WN, int KS, int R, bool LOOSE, bool WG, typename T>
 hipError_t launch_tile(const MmLaunch& a, hipStream_t st) {
   using G = Tile<A8, B8, MI, NI, WN, KS, R, WG>;
@@ -787,9 +804,8 @@ hipError_t launch_tile(const MmLaunch& a, hipStream_t st) {
                             : a.offsets ? most_tiles(a.rows, a.groups, G::BM)
                                         : (a.rows + G::BM - 1) / G::BM;
   auto k = mm_tile_kernel<A8, B8, EXACT, MI, NI, WN, KS, R, LOOSE, WG, T>;
-  static const hipError_t set =
-      hipFuncSetAttribute(reinterpret_cast<const void*>(k), hipFuncAttributeMaxDynamicSharedMemorySize, G::Lds);
-  if (set != hipSuccess) return set;
+  static std::atomic<uint64_t> set{0};  // bit d: on device d
+  if (const hipError_t e = allow_lds(reinterpret_cast<const void*>(k), G::Lds, set); e != hipSuccess) return e;
   const int64_t tiles = row_tiles * col_tiles, most = kCUs * (2 * G::Lds <= 160 * 1024 ? 2 : 1);
   k<<<dim3((uint32_t)(tiles < most ? tiles : most)), G::Threads, G::Lds, st>>>(a, (int)col_tiles);
   return hipGetLastError();

@@ -1,6 +1,7 @@
 """Which kernel a call of the products takes, without a GPU (tests/hip_recorder.py)."""
 import pytest
 
+from mxfp4_microscaling_quantization_amd import mxq
 from tests.hip_recorder import record
 
 BASE = 0x10000  # a 16-byte aligned, never dereferenced address
@@ -38,3 +39,19 @@ def test_scales_that_start_off_a_dword_take_no_dword_loads(fmt, fp32, tmp_path):
         args_of = call[3]
         assert args[LOOSE] == bool((args_of[1] | args_of[4]) % 4), call
     assert len(sides) == 3
+
+
+def test_lds_limit_on_every_device(tmp_path):
+    """A kernel with more than 64 KiB of LDS needs its limit raised once on each device that it runs
+    on, and again where that failed."""
+    devices = [0, 0, 3, 0, 3, 63, 63, 64, 70, 64]
+    got = record([gemm(4130, 4100, 512, device=d) for d in devices], tmp_path)
+    seen = set()
+    for d, (status, launches, attributes) in zip(devices, got):
+        assert status == mxq.MXQ_OK and [x[0] for x in launches] == [d] and launches[0][4] > 65536
+        due = d >= 64 or d not in seen
+        assert attributes == ([(d, launches[0][1], launches[0][4])] if due else [])
+        seen.add(d)
+    got = record([gemm(4130, 4100, 512, failures=f) for f in (1, 0, 0)], tmp_path)
+    assert [(status, len(launches), len(attributes)) for status, launches, attributes in got] == [
+        (mxq.MXQ_EHIP, 0, 0), (mxq.MXQ_OK, 1, 1), (mxq.MXQ_OK, 1, 0)]
