@@ -8,19 +8,25 @@ namespace {
 
 constexpr int kCols = 512;  // columns of a workgroup: 64 lanes of 8
 
-// act'(z) and, for SWIGLU, both halves of a pair (gate g, up u).
+// act'(z) and, for SWIGLU, both halves of a pair (gate g, up u). Far from zero s is 0 or 1 exactly
+// (for gelu from |z| = 11 on, for silu's from 89 on) and so is the slope: the polynomials that s
+// (1 - s) holds down there take z clamped, or they would be infinite and their products with
+// zero NaN. s itself takes z as it is, so NaN stays NaN.
+constexpr float kGeluFar = 16.0f, kSiluFar = 128.0f;
+__device__ __forceinline__ float silu_slope(float z, float s) {
+  return s * fmaf(__builtin_amdgcn_fmed3f(z, -kSiluFar, kSiluFar), 1.0f - s, 1.0f);
+}
+
 __device__ __forceinline__ float act_grad_f(float dy, float z, int act) {
   switch (act) {
     case kActRelu: return z > 0.0f ? dy : 0.0f;
     case kActGelu: {
       // d/dz [z s(w)], w = A z + B z^3: s + z s (1 - s) (A + 3 B z^2)
-      const float zz = z * z, s = sigmoid_f(z * fmaf(kGeluB, zz, kGeluA));
-      return dy * fmaf(z * s * (1.0f - s), fmaf(3.0f * kGeluB, zz, kGeluA), s);
+      const float near = __builtin_amdgcn_fmed3f(z, -kGeluFar, kGeluFar), zz = near * near;
+      const float s = sigmoid_f(z * fmaf(kGeluB, zz, kGeluA));
+      return dy * fmaf(near * s * (1.0f - s), fmaf(3.0f * kGeluB, zz, kGeluA), s);
     }
-    case kActSilu: {
-      const float s = sigmoid_f(z);
-      return dy * (s * fmaf(z, 1.0f - s, 1.0f));
-    }
+    case kActSilu: return dy * silu_slope(z, sigmoid_f(z));
   }
   return dy;
 }
@@ -103,7 +109,7 @@ __global__ __launch_bounds__(256) void act_grad_kernel(ActGradLaunch p, int col_
           for (int i = 0; i < 4; ++i) {
             const float g = (float)zr[u].v[2 * i], up = (float)zr[u].v[2 * i + 1], d = (float)dr[u].v[i];
             const float sg = sigmoid_f(g);
-            v[2 * i] = d * up * (sg * fmaf(g, 1.0f - sg, 1.0f));
+            v[2 * i] = d * up * silu_slope(g, sg);
             v[2 * i + 1] = d * (g * sg);
           }
         } else {
