@@ -180,6 +180,8 @@ hipError_t launch_waves(const MmLaunch& a, hipStream_t st) {
   const dim3 grid((uint32_t)(row_tiles * col_tiles));
   if (a.ep.out_f32)
     mm_rows_kernel<A8, B8, MT, NT, W, D, float><<<grid, 64 * W, 0, st>>>(a, (int)col_tiles);
+  else if constexpr (A8 && B8 && MT == 2)
+    return hipErrorInvalidValue;  // launch_gemm sends these to the tiles
   else
     mm_rows_kernel<A8, B8, MT, NT, W, D, __bf16><<<grid, 64 * W, 0, st>>>(a, (int)col_tiles);
   return hipGetLastError();

@@ -2,7 +2,8 @@
 import pytest
 
 from mxfp4_microscaling_quantization_amd import mxq
-from tests.hip_recorder import record
+from tests import mm_variants
+from tests.hip_recorder import kernels, record
 
 BASE = 0x10000  # a 16-byte aligned, never dereferenced address
 
@@ -55,3 +56,28 @@ def test_lds_limit_on_every_device(tmp_path):
     got = record([gemm(4130, 4100, 512, failures=f) for f in (1, 0, 0)], tmp_path)
     assert [(status, len(launches), len(attributes)) for status, launches, attributes in got] == [
         (mxq.MXQ_EHIP, 0, 0), (mxq.MXQ_OK, 1, 1), (mxq.MXQ_OK, 1, 0)]
+
+
+ACTS = ("none", "relu", "gelu", "silu", "swiglu")
+
+
+def variant_calls():
+    for counts, n, k, fmt, fp32, first, is_grouped in mm_variants.PRODUCTS:
+        kw = dict(fmt=fmt, fp32=fp32, a_scales=BASE + first * (fmt[0] == "4"), b_scales=BASE + first * (fmt[1] == "4"))
+        yield grouped(sum(counts), n, k, len(counts), **kw) if is_grouped else gemm(sum(counts), n, k, **kw)
+    for counts, n, k, fp32 in mm_variants.WGRADS:
+        yield (0, 0, "mxq_grouped_wgrad", [BASE, BASE, 1024, 1024, BASE, BASE, 1024, 1024, sum(counts), n, k, BASE,
+                                           len(counts), None, BASE, int(fp32), None])
+    for counts, n, act, fp32, bias, is_grouped in mm_variants.ACT_GRADS:
+        yield (0, 0, "mxq_act_grad", [BASE, BASE, int(fp32), sum(counts), n, ACTS.index(act), BASE if is_grouped else None,
+                                      len(counts), BASE, BASE if bias else None, BASE if bias else None, None])
+
+
+def test_every_compiled_kernel_is_among_the_tested_calls(tmp_path):
+    """No kernel of the products that no call reaches, and none that the GPU tests leave out."""
+    compiled = {k for k in kernels(tmp_path) if k[0].startswith(("mm_", "act_grad"))}
+    reached = set()
+    for status, launches, _ in record(list(variant_calls()), tmp_path):
+        assert status == mxq.MXQ_OK and launches
+        reached |= {launch[1] for launch in launches}
+    assert reached == compiled, compiled ^ reached
