@@ -22,3 +22,15 @@ def test_scale_pitch_of_the_weight_gradient(tmp_path):
     cases += [((a, b, 0), s) for (a, b), s in cases]
     got = record([wgrad(*c) for c, _ in cases], tmp_path)
     assert [(status, len(launches)) for status, launches, _ in got] == [(s, int(s == mxq.MXQ_OK)) for _, s in cases]
+
+
+@pytest.mark.parametrize("rows,n,experts", [(1, 8, 1), (64, 8, 1), (65, 8, 1), (64, 1024, 3), (65, 1024, 64), (300, 10, 7),
+                                            (5, 10, 9), (131071, 512, 5), (131072, 512, 5), (131072, 512, 4096),
+                                            (66000, 1040, 1), (2 ** 24, 8, 4096)])
+def test_workspace_of_the_activation_gradient(rows, n, experts):
+    """Room for the sums of every block of any split of the rows: a group of c rows has
+    ceil(c / each) blocks, most in all where every group has one row over whole blocks."""
+    each = 64 if rows <= 64 else 16 if rows * -(-n // 512) < 131072 else 128
+    groups = min(rows, experts)
+    most = groups + (rows - groups) // each
+    assert mxq.lib().mxq_act_grad_workspace(rows, n, experts) >= most * n * 4
