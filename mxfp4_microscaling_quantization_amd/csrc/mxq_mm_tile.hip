@@ -13,8 +13,9 @@ constexpr int kCUs = 256;  // of an MI355X; the tiles' LDS leaves room for one w
 // A workgroup of 2 x WN waves owns 64 MI x 32 NI WN results, a wave 32 MI x 32 NI. The
 // contraction runs in steps of 64 elements, four to a turn of 256. Each operand has R
 // slots in LDS with 128 bytes of every row in each, a whole cache line: a turn of an
-// MXFP4 row or half a turn of an FP8 row. (Direct loads of 1 KiB take 28 cycles as 8 rows
-// of 128 bytes, 36 as 16 rows of 64.) A slot is filled again from the moment when every
+// MXFP4 row or half a turn of an FP8 row. (A CU's direct loads of 1 KiB take 18 cycles each as
+// 8 rows of 128 bytes, 36 as 16 rows of 64, with all CUs at work on data in the L2s; 16 of
+// either alone.) A slot is filled again from the moment when every
 // wave has read its last fragments, the loads spread over the steps. Fragments of the next
 // step are read from LDS while the matrix cores work on the current one; one barrier a
 // slot is all that the waves wait for.
