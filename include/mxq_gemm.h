@@ -91,7 +91,9 @@ mxq_status mxq_grouped_gemm(const uint8_t* a, const void* a_scales, mxq_operand 
  *   d[e][i][j] = add[e][i][j] + sum over the tokens t of expert e of Y[t][i] X[t][j],
  * both operands as mxq_fp4_row_to_fp8_col writes them: E4M3 columns y [n, ld_y] and
  * x [k, ld_x], fp32 power-of-two scales y_scales [n, ld_ys] and x_scales [k, ld_xs],
- * one per 128-token group of an expert.
+ * one per 128-token group of an expert. Of a column, tokens from rows (rounded up to 16)
+ * on and scales from (rows + 127 n_experts) / 128 on are not read: both operands may be
+ * slices of wider tensors.
  * add, d: [n_experts, n, k] of d_dt; add may be NULL (zero) or d itself. An expert
  * without tokens gives add, or zeros; so does rows == 0.
  * offsets as in mxq_grouped_gemm. rows <= ld_y, ld_x <= 2^23, multiples of 16;

@@ -215,6 +215,9 @@ __global__ __launch_bounds__(128 * WN * KS, MI * NI > 8 ? 1 : 2) void mm_tile_ke
   const int64_t abytes = WG ? p.ld_a : A8 ? p.k : p.k / 2, bbytes = WG ? p.ld_b : B8 ? p.k : p.k / 2;
   const int64_t asbytes = WG ? 4 * p.ld_as : A8 ? p.k / 128 * 4 : p.k / 32;
   const int64_t bsbytes = WG ? 4 * p.ld_bs : B8 ? p.k / 128 * 4 : p.k / 32;
+  // weight gradient: bytes and scales that a column has at most
+  const int64_t col_bytes = (p.rows + 15) / 16 * 16;
+  const int col_scales = (int)((p.rows + 127 * (int64_t)p.groups) / 128);
   const uint32_t apitch = (uint32_t)(16 * abytes), bpitch = (uint32_t)(16 * bbytes);
   const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)lds;
 
@@ -261,12 +264,13 @@ __global__ __launch_bounds__(128 * WN * KS, MI * NI > 8 ? 1 : 2) void mm_tile_ke
     arows = (int)(aleft < G::BM ? aleft : G::BM);
     brows = (int)(bleft < G::BN ? bleft : G::BN);
     const int64_t from = WG ? s.begin - shift : 0;  // bytes of a row before the first piece
-    abuf = buffer_of(p.a + arow0 * abytes + from, arows * abytes - from);
-    bbuf = buffer_of(p.b + brow0 * bbytes + from, brows * bbytes - from);
+    // (of the last column no more than it has: it may end a wider tensor)
+    abuf = buffer_of(p.a + arow0 * abytes + from, (arows - 1) * abytes + (WG ? col_bytes : abytes) - from);
+    bbuf = buffer_of(p.b + brow0 * bbytes + from, (brows - 1) * bbytes + (WG ? col_bytes : bbytes) - from);
     ascale = static_cast<const uint8_t*>(p.a_scales) + arow0 * asbytes;
     bscale = static_cast<const uint8_t*>(p.b_scales) + brow0 * bsbytes;
-    asbuf = buffer_of(ascale, arows * asbytes);
-    bsbuf = buffer_of(bscale, brows * bsbytes);
+    asbuf = buffer_of(ascale, (arows - 1) * asbytes + (WG ? 4 * col_scales : asbytes));
+    bsbuf = buffer_of(bscale, (brows - 1) * bsbytes + (WG ? 4 * col_scales : bsbytes));
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
       const int arow = (wave * G::DA + j) * 8 + lane / 8, brow = (wave * G::DB + j) * 8 + lane / 8;
@@ -415,7 +419,7 @@ __global__ __launch_bounds__(128 * WN * KS, MI * NI > 8 ? 1 : 2) void mm_tile_ke
     asm volatile("" : "+v"(l));  // (addresses formed here, not held over the turns)
     const int want = 4 * c + (l & 3), most = halves - 1;
     int dword = first_slot + (want < most ? want : most);
-    if (WG) dword = dword < p.ld_as && dword < p.ld_bs ? dword : 0;  // malformed offsets stay inside
+    if (WG) dword = dword < col_scales ? dword : 0;  // malformed offsets stay inside
 #pragma unroll
     for (int j = 0; j < G::SLoads; ++j) {
       const int first = (wave * G::SLoads + j) * 16;  // uniform: 16 rows of A or of B

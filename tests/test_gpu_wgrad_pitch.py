@@ -48,3 +48,27 @@ def test_beyond():
     for a, b in (((yq, wide(ys, MOST + 1)), x), (x, (yq, wide(ys, 2 ** 23)))):
         with pytest.raises(mxq.MxqError):
             mxq.mxq_grouped_wgrad(a, b, off, 100)
+
+
+@pytest.mark.parametrize("counts,n,k", [([130, 33, 0, 257], 130, 328), ([300, 47], 700, 4200), ([7, 1], 40, 64),
+                                        ([130, 33, 0, 257], 700, 4200)])
+def test_slices_of_wider_tensors(counts, n, k):
+    """Columns and scales that end their tensors' rows: no more of the last row is there than its own."""
+    require_gpu()
+    rng = np.random.default_rng(n)
+    rows, slots = sum(counts), (sum(counts) + 127 * len(counts)) // 128
+    y, x = (gpu(*columns(rng, c, counts)) for c in (n, k))
+    off = torch.tensor([0, *np.cumsum(counts)], device="cuda:0")
+
+    def ending(t, width, before):
+        """The first `width` columns of t as the last ones of a tensor `before` columns wider."""
+        out = torch.full((t.shape[0], before + width), 0x7F if t.dtype == torch.uint8 else float("nan"), dtype=t.dtype,
+                         device=t.device)
+        out[:, before:] = t[:, :width]
+        return out[:, before:]
+
+    tokens = (rows + 15) // 16 * 16
+    for dtype in (torch.bfloat16, torch.float32):
+        want = mxq.mxq_grouped_wgrad(y, x, off, rows, out_dtype=dtype)
+        sliced = [(ending(q, tokens, 16 * b), ending(s, slots, b)) for (q, s), b in ((y, 1), (x, 5))]
+        assert torch.equal(mxq.mxq_grouped_wgrad(*sliced, off, rows, out_dtype=dtype), want)
