@@ -70,9 +70,9 @@ __device__ __forceinline__ float scale_part(const Part<FP8>& p, int s) {
 // One workgroup: 16 MT rows of one segment, 16 NT columns. Its W waves share the chunks
 // out in turn, D of a wave in flight together, and their sums are added in wave order
 // through LDS (so equal inputs give equal bits).
-// Bound by the weight's bytes where there are many (512 rows over 64 experts of 4096 x 7168:
-// 1.0 GB in 178 us, 5.6 TB/s), by a wave's latencies and the launch where there are few (one row of
-// 4096 x 14336: 31 MB in 8.8 us).
+// Bound by the weight's bytes where there are many (8 rows for each of 64 experts of 4096 x 7168:
+// 1.0 GB in 201 us, 5.0 TB/s; 512 rows of which about 50 of them have any: 0.8 GB in 175 us), by a
+// wave's latencies and the launch where there are few (one row of 4096 x 14336: 31 MB in 9 us).
 template <bool A8, bool B8, int MT, int NT, int W, int D, typename T>
 __global__ __launch_bounds__(64 * W, 1) void mm_rows_kernel(MmLaunch p, int col_tiles) {
   __shared__ float sums[W][MT * 16][NT * 16 + 4];
@@ -192,7 +192,7 @@ hipError_t launch_waves(const MmLaunch& a, hipStream_t st) {
 // pass over the chip fewer times (us, MXFP4, one row of n x k; 16 columns and 4, 8, 16 waves:
 // 4096 x 14336 16.3, 12.2, 10.5; 4096 x 4096 5.9, 5.3, 5.6; 16 columns and 4 waves, 32 and 8,
 // 64 and 4: 14336 x 4096 11.0, 10.1, 13.8; 28672 x 4096 19.8, 17.8, 17.0; 64 experts of
-// 4096 x 7168 for 512 rows 238, 206, 184.5, which is 5.4 TB/s).
+// 4096 x 7168 for 512 rows 238, 206, 184.5).
 // More rows: 32 x 32 results, so that a row of A is read for 32 columns
 // (64 rows of 4096 x 4096: 9.0 us; 32 x 16 results 12.5, 64 x 32 11.3).
 template <bool A8, bool B8>

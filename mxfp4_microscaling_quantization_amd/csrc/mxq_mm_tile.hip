@@ -26,13 +26,15 @@ constexpr int kCUs = 256;  // of an MI355X; the tiles' LDS leaves room for one w
 // workgroup on the CU instead (and gained nothing from a ring of eight slots, and up to a
 // tenth from two groups at FP4).
 // What bounds it: large tiles, the matrix cores under the chip's power limit while they run
-// (8192 x 8192 x 16384: MXFP4 4.3 PFLOP/s, where a loop of its products alone reaches 6.2 to 6.9
+// (8192 x 8192 x 16384: MXFP4 4.2 PFLOP/s, where a loop of its products alone reaches 6.2 to 6.9
 // on such data; FP8 2.4 of 4.2), and the results' bytes between (8192 x 14336 x 4096 MXFP4
-// to bf16 262 us, with GELU 281, with bias, GELU and z 312; to fp32 on a residual 374).
+// to bf16 275 us, with GELU 291, with bias, GELU and z 335; to fp32 on a residual 389). The
+// exact products of FP8 operands to fp32, on bf16 instructions, take 882 us there (MXFP4 weights 850).
 // Tiles of 128 and 64: the 1 KiB loads of a CU, at 18 cycles each, and one turn's latency
-// (256 x 4096 x 14336: MXFP4 25 us, FP8 31).
-// Weight gradient of 16 uneven experts, 16384 tokens, 2048 x 7168: 511 us, of which the
-// results are 470 MB; 13 us of every tile are its start and its results, 4.0 us a turn.
+// (256 x 4096 x 14336: MXFP4 26 us, FP8 33); with LOOSE scales the wait ahead of park_scales is for
+// all loads, so every second turn empties the ring (777 x 1336 x 4128 to fp32: 19 us).
+// Weight gradient of 16 uneven experts, 16384 tokens, 2048 x 7168: 509 us, of which the
+// results are 470 MB (accumulated in fp32: 990); 13 us of every tile are its start and its results, 4.0 us a turn.
 template <bool A8, bool B8, int MI, int NI, int WN, int KS, int R, bool WG>
 struct Tile {
   static constexpr int Waves = 2 * WN * KS, Threads = 64 * Waves;

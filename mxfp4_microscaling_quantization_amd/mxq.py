@@ -65,8 +65,9 @@ def lib() -> ctypes.CDLL:
     L.mxq_act_grad.argtypes = [vp, vp, i32, i64, i64, i32, vp, i64, vp, vp, vp, vp]
     L.mxq_act_grad_workspace.argtypes = [i64, i64, i64]
     L.mxq_act_grad_workspace.restype = i64
-    for name in ("mxq_gemm", "mxq_grouped_gemm", "mxq_grouped_wgrad", "mxq_act_grad", "mxq_quantize", "mxq_rht_quantize", "mxq_rht_quantize_mask", "mxq_dequantize", "mxq_fp8_to_mxfp4",
-                 "mxq_mxfp4_to_fp8", "mxq_fp4_row_to_fp8_col", "mxq_rht_apply", "mxq_amax", "mxq_rht_amax"):
+    for name in ("mxq_gemm", "mxq_grouped_gemm", "mxq_grouped_wgrad", "mxq_act_grad", "mxq_quantize", "mxq_rht_quantize",
+                 "mxq_rht_quantize_mask", "mxq_dequantize", "mxq_fp8_to_mxfp4", "mxq_mxfp4_to_fp8",
+                 "mxq_fp4_row_to_fp8_col", "mxq_rht_apply", "mxq_amax", "mxq_rht_amax"):
         getattr(L, name).restype = i32
     _lib = L
     return L
@@ -96,7 +97,8 @@ def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
 
 
 def _stream() -> int:
-    # the current device's current stream, without building a Stream object for it
+    # The current device's current stream by the functions under torch.cuda.current_stream(),
+    # which builds a Stream object around it: 0.2 us instead of 2.8, where a small call takes 9.
     return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
 
 
