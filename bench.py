@@ -47,8 +47,8 @@ SOURCES = ("include/mxq.h", "mxfp4_microscaling_quantization_amd/csrc")
 
 
 def source_digest() -> str:
-    """SHA-256 over the sources of the kernels measured here (the matrix products' are not
-    among them): PMC figures are reported only for the version the counters were taken on."""
+    """SHA-256 over the sources of the kernels measured here (the matrix products' and
+    those around them are not among them): PMC figures are reported only for the version the counters were taken on."""
     import hashlib
 
     h = hashlib.sha256()
@@ -57,7 +57,7 @@ def source_digest() -> str:
         p = os.path.join(ROOT, rel)
         if os.path.isdir(p):
             paths += sorted(os.path.join(p, f) for f in os.listdir(p)
-                            if f.endswith((".hip", ".h")) and not f.startswith(("mxq_mm", "mxq_act_grad")))
+                            if f.endswith((".hip", ".h")) and not f.startswith(("mxq_mm", "mxq_act_grad", "mxq_moe")))
         else:
             paths.append(p)
     for p in paths:

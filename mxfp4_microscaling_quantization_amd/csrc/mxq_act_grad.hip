@@ -1,6 +1,7 @@
 // The gradient of the products' epilogue: dz = act'(z) dy and its column sums per
-// group of rows (the bias gradient).
+// group of rows (the bias gradient), from z as it was or as it was kept in FP8.
 #include "mxq_mm.h"
+#include "mxq_moe_fp8.h"
 
 namespace mxq {
 
@@ -54,7 +55,11 @@ struct Run {
     }
   }
   __device__ __forceinline__ void store(T* p, int64_t left) const {
-    if constexpr (VEC) {
+    if constexpr (VEC && sizeof(v) == 8) {
+      uint2 x;
+      __builtin_memcpy(&x, v, 8);
+      store_nt(reinterpret_cast<uint2*>(p), x);
+    } else if constexpr (VEC) {
 #pragma unroll
       for (int i = 0; i < (int)sizeof(v) / 16; ++i) {
         uint4 x;
@@ -69,13 +74,48 @@ struct Run {
   }
 };
 
+// Eight neighbouring values of z: as they are, or E4M3 under the scale of their 128 columns.
+template <typename T, bool VEC>
+struct ZRun {
+  Run<T, 8, VEC> run;
+  __device__ __forceinline__ void load(const ActGradLaunch& p, int64_t row, int64_t col, int64_t left) {
+    run.load(static_cast<const T*>(p.z) + row * p.n + col, left);
+  }
+  __device__ __forceinline__ void values(float (&v)[8]) const {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = (float)run.v[i];
+  }
+};
+template <bool VEC>
+struct ZRun8 {
+  uint2 q;
+  uint32_t scale;
+  __device__ __forceinline__ void load(const ActGradLaunch& p, int64_t row, int64_t col, int64_t left) {
+    const uint8_t* z = static_cast<const uint8_t*>(p.z) + row * p.n + col;
+    scale = as_u(p.z_scales[row * ((p.n + 127) / 128) + col / 128]);
+    if constexpr (VEC) {
+      q = load_nt(reinterpret_cast<const uint2*>(z));
+    } else {
+      uint8_t b[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) b[i] = i < left ? z[i] : 0;
+      __builtin_memcpy(&q, b, 8);
+    }
+  }
+  __device__ __forceinline__ void values(float (&v)[8]) const {
+    const float s = fp8_scale(scale);
+    const f32x2_t a = __builtin_amdgcn_cvt_pk_f32_fp8((int)q.x, false), b = __builtin_amdgcn_cvt_pk_f32_fp8((int)q.x, true);
+    const f32x2_t c = __builtin_amdgcn_cvt_pk_f32_fp8((int)q.y, false), d = __builtin_amdgcn_cvt_pk_f32_fp8((int)q.y, true);
+    v[0] = a.x * s; v[1] = a.y * s; v[2] = b.x * s; v[3] = b.y * s;
+    v[4] = c.x * s; v[5] = c.y * s; v[6] = d.x * s; v[7] = d.y * s;
+  }
+};
+
 // One workgroup: up to p.block_rows rows of one group, 512 columns. Its waves take every
 // fourth row, four of them in flight: their loads go ahead of the first one's arithmetic.
-// The sums of the four waves are added in order through LDS.
-// Bound by memory: 65536 x 4096 bf16 swiglu with its sums moves 1.34 GB in 255 us, 5.3 TB/s, what a
-// plain stream that reads twice what it writes reaches here.
-template <typename T, bool SUM, bool GATED, bool VEC>
-__global__ __launch_bounds__(256) void act_grad_kernel(ActGradLaunch p, int col_tiles) {
+// The sums of the four waves are added in order through LDS. H: act(z) goes out as well.
+template <typename T, typename Z, bool SUM, bool GATED, bool VEC, bool H>
+__device__ __forceinline__ void grad_block(const ActGradLaunch& p, int col_tiles) {
   __shared__ float sums[4][kCols];
   constexpr int U = 4;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -88,33 +128,41 @@ __global__ __launch_bounds__(256) void act_grad_kernel(ActGradLaunch p, int col_
   float sum[8] = {};
   if (left > 0) {
     const int64_t dn = GATED ? p.n / 2 : p.n;
-    const T* z = static_cast<const T*>(p.z) + (s.begin + first) * p.n + col;
-    const T* dy = static_cast<const T*>(p.dy) + (s.begin + first) * dn + (GATED ? col / 2 : col);
+    const int64_t from = (s.begin + first) * dn + (GATED ? col / 2 : col);
+    const T* dy = static_cast<const T*>(p.dy) + from;
     T* dz = static_cast<T*>(p.dz) + (s.begin + first) * p.n + col;
+    T* h = H ? static_cast<T*>(p.h) + from : nullptr;
     for (int r0 = wave; r0 < count; r0 += 4 * U) {
-      Run<T, 8, VEC> zr[U];
+      Z zr[U];
       Run<T, GATED ? 4 : 8, VEC> dr[U];
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         const int64_t row = r0 + 4 * u < count ? r0 + 4 * u : count - 1;
-        zr[u].load(z + row * p.n, left);
+        zr[u].load(p, s.begin + first + row, col, left);
         dr[u].load(dy + row * dn, GATED ? left / 2 : left);
       }
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         if (r0 + 4 * u >= count) break;
-        float v[8];
+        float z[8], v[8];
+        Run<T, GATED ? 4 : 8, VEC> ho;
+        zr[u].values(z);
         if constexpr (GATED) {
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const float g = (float)zr[u].v[2 * i], up = (float)zr[u].v[2 * i + 1], d = (float)dr[u].v[i];
+            const float g = z[2 * i], up = z[2 * i + 1], d = (float)dr[u].v[i];
             const float sg = sigmoid_f(g);
             v[2 * i] = d * up * silu_slope(g, sg);
             v[2 * i + 1] = d * (g * sg);
+            if constexpr (H) ho.v[i] = (T)(g * sg * up);
           }
         } else {
 #pragma unroll
-          for (int i = 0; i < 8; ++i) v[i] = act_grad_f((float)dr[u].v[i], (float)zr[u].v[i], p.act);
+          for (int i = 0; i < 8; ++i) v[i] = act_grad_f((float)dr[u].v[i], z[i], p.act);
+          if constexpr (H) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) ho.v[i] = (T)act_f(z[i], p.act);
+          }
         }
         Run<T, 8, VEC> o;
 #pragma unroll
@@ -123,6 +171,7 @@ __global__ __launch_bounds__(256) void act_grad_kernel(ActGradLaunch p, int col_
           o.v[i] = (T)v[i];
         }
         o.store(dz + (int64_t)(r0 + 4 * u) * p.n, left);
+        if constexpr (H) ho.store(h + (int64_t)(r0 + 4 * u) * dn, GATED ? left / 2 : left);
       }
     }
   }
@@ -135,6 +184,18 @@ __global__ __launch_bounds__(256) void act_grad_kernel(ActGradLaunch p, int col_
       if (at < p.n) p.partials[(int64_t)block * p.n + at] = (sums[0][c] + sums[1][c]) + (sums[2][c] + sums[3][c]);
     }
   }
+}
+
+// Bound by memory: 65536 x 4096 bf16 swiglu with its sums moves 1.34 GB in 255 us, 5.3 TB/s, what a
+// plain stream that reads twice what it writes reaches here.
+template <typename T, bool SUM, bool GATED, bool VEC>
+__global__ __launch_bounds__(256) void act_grad_kernel(ActGradLaunch p, int col_tiles) {
+  grad_block<T, ZRun<T, VEC>, SUM, GATED, VEC, false>(p, col_tiles);
+}
+
+template <typename T, bool SUM, bool GATED, bool VEC, bool H>
+__global__ __launch_bounds__(256) void fp8_act_grad_kernel(ActGradLaunch p, int col_tiles) {
+  grad_block<T, ZRun8<VEC>, SUM, GATED, VEC, H>(p, col_tiles);
 }
 
 // db[g] = the partial sums of the group's row blocks. A column has kLanes threads, each with
@@ -165,14 +226,30 @@ __global__ __launch_bounds__(64 * kLanes) void act_grad_sum_kernel(ActGradLaunch
 }
 
 template <typename T, bool SUM, bool GATED>
-void launch_rows(const ActGradLaunch& a, dim3 grid, int col_tiles, hipStream_t st) {
-  if (a.n % 8 == 0)
-    act_grad_kernel<T, SUM, GATED, true><<<grid, 256, 0, st>>>(a, col_tiles);
-  else
-    act_grad_kernel<T, SUM, GATED, false><<<grid, 256, 0, st>>>(a, col_tiles);
-}
+struct Rows {
+  static void launch(const ActGradLaunch& a, dim3 grid, int col_tiles, hipStream_t st) {
+    if (a.n % 8 == 0)
+      act_grad_kernel<T, SUM, GATED, true><<<grid, 256, 0, st>>>(a, col_tiles);
+    else
+      act_grad_kernel<T, SUM, GATED, false><<<grid, 256, 0, st>>>(a, col_tiles);
+  }
+};
+template <typename T, bool SUM, bool GATED>
+struct Fp8Rows {
+  template <bool VEC>
+  static void launch_v(const ActGradLaunch& a, dim3 grid, int col_tiles, hipStream_t st) {
+    if (a.h)
+      fp8_act_grad_kernel<T, SUM, GATED, VEC, true><<<grid, 256, 0, st>>>(a, col_tiles);
+    else
+      fp8_act_grad_kernel<T, SUM, GATED, VEC, false><<<grid, 256, 0, st>>>(a, col_tiles);
+  }
+  static void launch(const ActGradLaunch& a, dim3 grid, int col_tiles, hipStream_t st) {
+    if (a.n % 8 == 0) launch_v<true>(a, grid, col_tiles, st);
+    else launch_v<false>(a, grid, col_tiles, st);
+  }
+};
 
-template <typename T>
+template <template <typename, bool, bool> class Kernel, typename T>
 hipError_t launch_t(ActGradLaunch a, hipStream_t st) {
   const int64_t col_tiles = (a.n + kCols - 1) / kCols, blocks = act_grad_blocks(a.rows, a.groups, a.block_rows);
   // one block of rows: its sums are the bias gradient
@@ -182,13 +259,13 @@ hipError_t launch_t(ActGradLaunch a, hipStream_t st) {
     const dim3 grid((uint32_t)(blocks * col_tiles));
     const bool gated = a.act == kActSwiglu;
     if (a.db && gated)
-      launch_rows<T, true, true>(a, grid, (int)col_tiles, st);
+      Kernel<T, true, true>::launch(a, grid, (int)col_tiles, st);
     else if (a.db)
-      launch_rows<T, true, false>(a, grid, (int)col_tiles, st);
+      Kernel<T, true, false>::launch(a, grid, (int)col_tiles, st);
     else if (gated)
-      launch_rows<T, false, true>(a, grid, (int)col_tiles, st);
+      Kernel<T, false, true>::launch(a, grid, (int)col_tiles, st);
     else
-      launch_rows<T, false, false>(a, grid, (int)col_tiles, st);
+      Kernel<T, false, false>::launch(a, grid, (int)col_tiles, st);
   }
   if (a.db && !direct) {
     const int64_t sum_tiles = (a.n + 63) / 64;
@@ -200,7 +277,10 @@ hipError_t launch_t(ActGradLaunch a, hipStream_t st) {
 }  // namespace
 
 hipError_t launch_act_grad(const ActGradLaunch& a, hipStream_t st) {
-  return a.f32 ? launch_t<float>(a, st) : launch_t<__bf16>(a, st);
+  return a.f32 ? launch_t<Rows, float>(a, st) : launch_t<Rows, __bf16>(a, st);
+}
+hipError_t launch_fp8_act_grad(const ActGradLaunch& a, hipStream_t st) {
+  return a.f32 ? launch_t<Fp8Rows, float>(a, st) : launch_t<Fp8Rows, __bf16>(a, st);
 }
 
 }  // namespace mxq

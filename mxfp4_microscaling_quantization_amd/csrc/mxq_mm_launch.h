@@ -59,6 +59,8 @@ struct ActGradLaunch {
   float* db;
   float* partials;
   int block_rows;
+  const float* z_scales;  // z in FP8 only: [rows, ceil(n / 128)]
+  void* h;                // z in FP8 only: act(z), or null
 };
 
 // Rows that one workgroup of the activation gradient sums: all of up to 64, whose sums then
@@ -76,5 +78,6 @@ constexpr int64_t act_grad_blocks(int64_t rows, int64_t groups, int64_t each) {
   return (rows + (each - 1) * groups) / each;
 }
 hipError_t launch_act_grad(const ActGradLaunch& a, hipStream_t st);
+hipError_t launch_fp8_act_grad(const ActGradLaunch& a, hipStream_t st);
 
 }  // namespace mxq

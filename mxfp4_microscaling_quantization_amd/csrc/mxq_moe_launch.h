@@ -1,0 +1,64 @@
+// Host-side launch interface of the operators around the experts' products.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+namespace mxq {
+
+struct RouteLaunch {
+  const void* logits;  // [tokens, experts], row stride ld
+  int f32;
+  int64_t tokens, ld;
+  int experts, top_k, renorm;
+  float* weights;  // [tokens, top_k]
+  int32_t* chosen;
+  const float* dw;  // gradient only
+  void* dlogits;    // gradient only: [tokens, experts]
+};
+hipError_t launch_route(const RouteLaunch& a, hipStream_t st);
+hipError_t launch_route_grad(const RouteLaunch& a, hipStream_t st);
+
+struct SortLaunch {
+  const int32_t* experts;  // [count]
+  int64_t count;
+  int n_experts;
+  int64_t* offsets;
+  int32_t *positions, *order;
+  int32_t* counts;  // workspace [blocks, n_experts], then [n_experts]
+};
+// Up to this many assignments one workgroup does everything in one launch.
+constexpr int64_t kSortOne = 4096;
+// Assignments of a block otherwise: as many as keep the table of counts at 1024 blocks at most.
+constexpr int64_t sort_chunk(int64_t count) {
+  return count <= 1024 * 2048 ? 2048 : (count + 1023) / 1024 + 255 & ~(int64_t)255;
+}
+constexpr int64_t sort_workspace(int64_t count, int64_t experts) {
+  return count <= kSortOne ? 0 : ((count + sort_chunk(count) - 1) / sort_chunk(count) + 1) * experts * 4;
+}
+hipError_t launch_expert_sort(const SortLaunch& a, hipStream_t st);
+
+// dispatch and combine: rows of tokens and rows of experts.
+struct RowsLaunch {
+  const void* x;  // dispatch: tokens; combine: experts' rows; gradient: of the tokens
+  int x_f32;
+  int64_t ldx;  // dispatch only
+  int64_t tokens, width, rows;
+  const int32_t* positions;
+  int top_k;
+  int fmt;  // dispatch only
+  const float* weights;
+  const void* res;  // combine: residual; gradient: experts' rows
+  void* out;        // dispatch, gradient: experts' rows; combine: tokens
+  int out_f32;
+  void* scales;  // dispatch only
+  float* dw;     // gradient only
+};
+hipError_t launch_dispatch(const RowsLaunch& a, hipStream_t st);
+hipError_t launch_combine(const RowsLaunch& a, hipStream_t st);
+hipError_t launch_combine_grad(const RowsLaunch& a, hipStream_t st);
+
+hipError_t launch_fp8_quantize(const void* x, int f32, int64_t rows, int64_t cols, int64_t ldx, uint8_t* q8,
+                               float* scales, hipStream_t st);
+
+}  // namespace mxq

@@ -65,7 +65,18 @@ def lib() -> ctypes.CDLL:
     L.mxq_act_grad.argtypes = [vp, vp, i32, i64, i64, i32, vp, i64, vp, vp, vp, vp]
     L.mxq_act_grad_workspace.argtypes = [i64, i64, i64]
     L.mxq_act_grad_workspace.restype = i64
-    for name in ("mxq_gemm", "mxq_grouped_gemm", "mxq_grouped_wgrad", "mxq_act_grad", "mxq_quantize", "mxq_rht_quantize",
+    L.mxq_route.argtypes = [vp, i32, i64, i64, i64, i64, i32, vp, vp, vp]
+    L.mxq_route_grad.argtypes = [vp, vp, vp, vp, i32, i64, i64, i64, i64, i32, vp, vp]
+    L.mxq_expert_sort.argtypes = [vp, i64, i64, vp, vp, vp, vp, vp]
+    L.mxq_expert_sort_workspace.argtypes = [i64, i64]
+    L.mxq_expert_sort_workspace.restype = i64
+    L.mxq_dispatch.argtypes = [vp, i32, i64, i64, i64, vp, i64, i64, i32, vp, vp, vp]
+    L.mxq_combine.argtypes = [vp, i32, i64, i64, vp, vp, i64, i64, vp, vp, i32, vp]
+    L.mxq_combine_grad.argtypes = [vp, i32, vp, i32, i64, i64, vp, vp, i64, i64, vp, vp, vp]
+    L.mxq_fp8_quantize.argtypes = [vp, i32, i64, i64, i64, vp, vp, vp]
+    L.mxq_fp8_act_grad.argtypes = [vp, i32, vp, vp, i64, i64, i32, vp, i64, vp, vp, vp, vp, vp]
+    for name in ("mxq_route", "mxq_route_grad", "mxq_expert_sort", "mxq_dispatch", "mxq_combine", "mxq_combine_grad",
+                 "mxq_fp8_quantize", "mxq_fp8_act_grad", "mxq_gemm", "mxq_grouped_gemm", "mxq_grouped_wgrad", "mxq_act_grad", "mxq_quantize", "mxq_rht_quantize",
                  "mxq_rht_quantize_mask", "mxq_dequantize", "mxq_fp8_to_mxfp4", "mxq_mxfp4_to_fp8",
                  "mxq_fp4_row_to_fp8_col", "mxq_rht_apply", "mxq_amax", "mxq_rht_amax"):
         getattr(L, name).restype = i32
@@ -441,3 +452,227 @@ def mxq_act_grad(dy: torch.Tensor, z: torch.Tensor, act: str = "none", offsets: 
     stream = _on_gpu(dy, z, dz, offsets, *((db, workspace) if bias_grad else ()))
     _check(lib().mxq_act_grad(dyp, zp, dt, rows, n, code, offp, groups, dzp, dbp, wsp, stream))
     return (dz, db) if bias_grad else dz
+
+
+# ---------------------------------------------------------------------------
+# Around the experts' products (include/mxq_moe.h). Assignment t k + j is token t's choice
+# j of top k; `positions` [T, k] holds the rows of the assignments (-1: none).
+
+_ROWS = {None: 0, "mxfp4": 1, "fp8": 2}
+
+
+def _strided_rows(t: torch.Tensor, what: str):
+    """(rows, columns, row stride) of a matrix whose columns lie side by side."""
+    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError(f"{what}: a matrix with unit column stride expected")
+    rows, cols = t.shape
+    # (a stride means nothing where there are fewer than two rows)
+    return rows, cols, t.stride(0) if rows > 1 else cols
+
+
+def _positions(positions: torch.Tensor):
+    if positions.dtype != torch.int32 or positions.dim() != 2 or not positions.is_contiguous():
+        raise ValueError("positions: dense int32 [tokens, top_k] expected")
+    return positions.shape
+
+
+def mxq_route(logits: torch.Tensor, top_k: int, renorm: bool = False, out=None):
+    """mxq_route: (weights fp32 [T, k], experts int32 [T, k]) of the top_k largest logits
+    [T, E] of every token, in falling order; weights by the softmax over all experts or,
+    with `renorm`, over the chosen ones. -Inf is never chosen: expert -1, weight 0."""
+    tokens, n_experts, ld = _strided_rows(logits, "logits")
+    dt = _float_code(logits.dtype)
+    shape = (tokens, top_k)
+    if out is None:
+        out = logits.new_empty(shape, dtype=torch.float32), logits.new_empty(shape, dtype=torch.int32)
+    weights, experts = out
+    wp, ep = _dense(weights, shape, torch.float32, "weights"), _dense(experts, shape, torch.int32, "experts")
+    stream = _on_gpu(logits, weights, experts)
+    _check(lib().mxq_route(logits.data_ptr(), dt, tokens, n_experts, ld, top_k, int(renorm), wp, ep, stream))
+    return weights, experts
+
+
+def mxq_route_grad(dw: torch.Tensor, weights: torch.Tensor, experts: torch.Tensor, logits: torch.Tensor,
+                   renorm: bool = False, out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """mxq_route_grad: the gradient of the logits [T, E] (their type, dense) from the
+    gradient `dw` of the weights that mxq_route gave for them."""
+    tokens, n_experts, ld = _strided_rows(logits, "logits")
+    dt, shape = _float_code(logits.dtype), dw.shape
+    if len(shape) != 2 or shape[0] != tokens:
+        raise ValueError(f"dw: [{tokens}, top_k] expected, got {tuple(shape)}")
+    dwp = _dense(dw, shape, torch.float32, "dw")
+    wp, ep = _dense(weights, shape, torch.float32, "weights"), _dense(experts, shape, torch.int32, "experts")
+    if out is None:
+        out = logits.new_empty((tokens, n_experts))
+    op = _dense(out, (tokens, n_experts), logits.dtype, "out")
+    stream = _on_gpu(logits, dw, weights, experts, out)
+    _check(lib().mxq_route_grad(dwp, wp, ep, logits.data_ptr(), dt, tokens, n_experts, ld, shape[1], int(renorm), op,
+                                stream))
+    return out
+
+
+class ExpertRows(NamedTuple):
+    offsets: torch.Tensor    # int64 [E + 1]: rows of every expert
+    positions: torch.Tensor  # int32, as the experts: the row of every assignment, or -1
+    order: torch.Tensor      # int32 [assignments]: the assignment of every row, -1 behind the last one
+
+
+def mxq_expert_sort(experts: torch.Tensor, n_experts: int, out: Optional[ExpertRows] = None,
+                    workspace: Optional[torch.Tensor] = None) -> ExpertRows:
+    """mxq_expert_sort: the rows of every expert from the choices `experts` (int32 [T, k];
+    values outside [0, n_experts) have no row), those of one expert in the tokens' order.
+    `workspace` (uint8, mxq_expert_sort_workspace bytes) is allocated if absent."""
+    ep, count = _dense(experts, experts.shape, torch.int32, "experts"), experts.numel()
+    if out is None:
+        out = ExpertRows(experts.new_empty((n_experts + 1,), dtype=torch.int64), torch.empty_like(experts),
+                         experts.new_empty((count,)))
+    offsets, positions, order = out
+    offp = _dense(offsets, (n_experts + 1,), torch.int64, "offsets")
+    pp, op = _dense(positions, experts.shape, torch.int32, "positions"), _dense(order, (count,), torch.int32, "order")
+    need = lib().mxq_expert_sort_workspace(count, n_experts)
+    if workspace is None:
+        workspace = experts.new_empty((need,), dtype=torch.uint8) if need else None
+    elif workspace.numel() * workspace.element_size() < need or not workspace.is_contiguous():
+        raise ValueError(f"dense workspace of {need} bytes expected")
+    stream = _on_gpu(experts, offsets, positions, order, workspace)
+    _check(lib().mxq_expert_sort(ep, count, n_experts, offp, pp, op, _ptr(workspace), stream))
+    return out
+
+
+def mxq_dispatch(x: torch.Tensor, positions: torch.Tensor, rows: Optional[int] = None, fmt: Optional[str] = None,
+                 out=None):
+    """mxq_dispatch: every token's row x [T, H] copied to the rows of its assignments; the
+    result has `rows` rows (T k if absent), of which those of no assignment are left as
+    they are. fmt None: rows as x; "mxfp4": (codes, e8m0), the bits of mxq_quantize;
+    "fp8": (E4M3, scales), the bits of mxq_fp8_quantize. The gradient is mxq_combine
+    without weights."""
+    tokens, width, ldx = _strided_rows(x, "x")
+    dt, code = _float_code(x.dtype), _ROWS[fmt]
+    if _positions(positions)[0] != tokens:
+        raise ValueError(f"positions of {positions.shape[0]} tokens for {tokens}")
+    if rows is None:
+        rows = positions.numel() if out is None else (out if code == 0 else out[0]).shape[0]
+    if code == 0:
+        if out is None:
+            out = x.new_empty((rows, width))
+        op, sp, given = _dense(out, (rows, width), x.dtype, "out"), None, (out,)
+    else:
+        per, block, kind = (2, 32, torch.uint8) if code == 1 else (1, 128, torch.float32)
+        if out is None:
+            out = (x.new_empty((rows, width // per), dtype=torch.uint8),
+                   x.new_empty((rows, width // block), dtype=kind))
+        op = _dense(out[0], (rows, width // per), torch.uint8, "codes")
+        sp, given = _dense(out[1], (rows, width // block), kind, "scales"), out
+    stream = _on_gpu(x, positions, *given)
+    _check(lib().mxq_dispatch(x.data_ptr(), dt, tokens, width, ldx, positions.data_ptr(), positions.shape[1], rows,
+                              code, op, sp, stream))
+    return out
+
+
+def mxq_combine(y: torch.Tensor, positions: torch.Tensor, weights: Optional[torch.Tensor] = None,
+                residual: Optional[torch.Tensor] = None, out_dtype=torch.bfloat16,
+                out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """mxq_combine: out [T, H] = residual + sum over j of weights[:, j] times the rows
+    y[positions[:, j]] (weights fp32 [T, k], 1 if absent; residual of the result's type, may
+    be `out` itself). Assignments without a row add nothing."""
+    tokens, _ = shape = _positions(positions)
+    rows, width = y.shape
+    if out is not None:
+        out_dtype = out.dtype
+    ydt, dt = _float_code(y.dtype), _float_code(out_dtype)
+    yp = _dense(y, (rows, width), y.dtype, "y")
+    wp = None if weights is None else _dense(weights, shape, torch.float32, "weights")
+    rp = None if residual is None else _dense(residual, (tokens, width), out_dtype, "residual")
+    if out is None:
+        out = y.new_empty((tokens, width), dtype=out_dtype)
+    op = _dense(out, (tokens, width), out_dtype, "out")
+    stream = _on_gpu(y, positions, weights, residual, out)
+    _check(lib().mxq_combine(yp, ydt, rows, width, positions.data_ptr(), wp, tokens, shape[1], rp, op, dt, stream))
+    return out
+
+
+def mxq_combine_grad(grad: torch.Tensor, y: torch.Tensor, positions: torch.Tensor,
+                     weights: Optional[torch.Tensor] = None, weight_grad: bool = True,
+                     out: Optional[torch.Tensor] = None, dw: Optional[torch.Tensor] = None):
+    """mxq_combine_grad: from the gradient `grad` [T, H] of mxq_combine's result the
+    gradient dy of its rows y [R, H] (y's type; rows of no assignment are left as they are)
+    and, with `weight_grad`, (dy, dw), dw fp32 [T, k] that of its weights. `out` may be y."""
+    tokens, _ = shape = _positions(positions)
+    rows, width = y.shape
+    gdt, ydt = _float_code(grad.dtype), _float_code(y.dtype)
+    gp, yp = _dense(grad, (tokens, width), grad.dtype, "grad"), _dense(y, (rows, width), y.dtype, "y")
+    wp = None if weights is None else _dense(weights, shape, torch.float32, "weights")
+    if out is None:
+        out = torch.empty_like(y)
+    op = _dense(out, (rows, width), y.dtype, "out")
+    dwp = None
+    if weight_grad:
+        if dw is None:
+            dw = grad.new_empty(shape, dtype=torch.float32)
+        dwp = _dense(dw, shape, torch.float32, "dw")
+    stream = _on_gpu(grad, y, positions, weights, out, dw if weight_grad else None)
+    _check(lib().mxq_combine_grad(gp, gdt, yp, ydt, rows, width, positions.data_ptr(), wp, tokens, shape[1], op, dwp,
+                                  stream))
+    return (out, dw) if weight_grad else out
+
+
+def mxq_fp8_quantize(x: torch.Tensor, out=None):
+    """mxq_fp8_quantize: (E4M3 uint8 [R, C], power-of-two fp32 scales [R, ceil(C / 128)]) of
+    x [R, C]: an operand of the products (C a multiple of 128), or z kept for
+    mxq_fp8_act_grad (any C)."""
+    rows, cols, ldx = _strided_rows(x, "x")
+    dt, groups = _float_code(x.dtype), (cols + 127) // 128
+    if out is None:
+        out = x.new_empty((rows, cols), dtype=torch.uint8), x.new_empty((rows, groups), dtype=torch.float32)
+    qp, sp = _dense(out[0], (rows, cols), torch.uint8, "codes"), _dense(out[1], (rows, groups), torch.float32, "scales")
+    stream = _on_gpu(x, *out)
+    _check(lib().mxq_fp8_quantize(x.data_ptr(), dt, rows, cols, ldx, qp, sp, stream))
+    return out
+
+
+def mxq_fp8_act_grad(dy: torch.Tensor, z8, act: str = "none", offsets: Optional[torch.Tensor] = None,
+                     bias_grad: bool = False, recompute: bool = False, out: Optional[torch.Tensor] = None,
+                     db: Optional[torch.Tensor] = None, h: Optional[torch.Tensor] = None,
+                     workspace: Optional[torch.Tensor] = None):
+    """mxq_fp8_act_grad: mxq_act_grad for a z that was kept as z8 = (E4M3 [R, N], scales
+    [R, ceil(N / 128)]) by mxq_fp8_quantize. Gives dz (dy's type), then db with `bias_grad`,
+    then h = act(z) with `recompute` (dy's type and shape; may be dy): a tuple where there
+    is more than dz."""
+    q8, scales = z8
+    if q8.dim() != 2:
+        raise ValueError("z8: a matrix of codes expected")
+    rows, n = shape = q8.shape
+    code, dtype = _ACT[act], dy.dtype
+    dt = _float_code(dtype)
+    qp = _dense(q8, shape, torch.uint8, "z8")
+    sp = _dense(scales, (rows, (n + 127) // 128), torch.float32, "z8's scales")
+    dy_shape = (rows, n // 2 if code == SWIGLU else n)
+    dyp = _dense(dy, dy_shape, dtype, "dy")
+    groups, offp = (1, None) if offsets is None else (_offsets(offsets), offsets.data_ptr())
+    if out is None:
+        out = dy.new_empty(shape)
+    dzp = _dense(out, shape, dtype, "out")
+    got, given = [out], [out]
+    dbp = wsp = hp = None
+    if bias_grad:
+        db_shape = (n,) if offsets is None else (groups, n)
+        if db is None:
+            db = dy.new_empty(db_shape, dtype=torch.float32)
+        dbp = _dense(db, db_shape, torch.float32, "db")
+        need = lib().mxq_act_grad_workspace(rows, n, groups)
+        if workspace is None:
+            workspace = dy.new_empty((need,), dtype=torch.uint8)
+        elif workspace.numel() * workspace.element_size() < need or not workspace.is_contiguous():
+            raise ValueError(f"dense workspace of {need} bytes expected")
+        wsp = workspace.data_ptr()
+        got.append(db)
+        given += [db, workspace]
+    if recompute:
+        if h is None:
+            h = torch.empty_like(dy)
+        hp = _dense(h, dy_shape, dtype, "h")
+        got.append(h)
+        given.append(h)
+    stream = _on_gpu(dy, q8, scales, offsets, *given)
+    _check(lib().mxq_fp8_act_grad(dyp, dt, qp, sp, rows, n, code, offp, groups, dzp, dbp, hp, wsp, stream))
+    return tuple(got) if len(got) > 1 else got[0]
