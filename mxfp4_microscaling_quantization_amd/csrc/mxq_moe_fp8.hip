@@ -49,18 +49,19 @@ __global__ __launch_bounds__(kThreads) void fp8_rows_kernel(Fp8Params p) {
   }
 #pragma unroll
   for (int u = 0; u < kUnroll; ++u) {
-    float v[8], scale;
+    float v[8];
+    uint32_t q[2], scale;
     to_f32(raw[u], v);
-    const uint2 q = fp8_encode8(v, scale);
+    fp8_encode<8, 16>(v, q, scale);
     uint8_t* to = p.q8 + row[u] * p.cols + col[u];
     if constexpr (VEC) {
-      if (left[u] > 0) *reinterpret_cast<uint2*>(to) = q;
+      if (left[u] > 0) *reinterpret_cast<uint2*>(to) = make_uint2(q[0], q[1]);
     } else {
 #pragma unroll
       for (int i = 0; i < 8; ++i)
-        if (i < left[u]) to[i] = (uint8_t)((i < 4 ? q.x : q.y) >> (8 * (i & 3)));
+        if (i < left[u]) to[i] = (uint8_t)(q[i >> 2] >> (8 * (i & 3)));
     }
-    if (left[u] > 0 && col[u] % 128 == 0) p.scales[row[u] * (p.cpr.d / 16) + col[u] / 128] = scale;
+    if (left[u] > 0 && col[u] % 128 == 0) p.scales[row[u] * (p.cpr.d / 16) + col[u] / 128] = as_f(scale);
   }
 }
 
