@@ -47,10 +47,9 @@ __device__ __forceinline__ float group_max(float v) {  // NaN if any is
 // does not grow with x. -Inf and far below: 0; NaN: NaN.
 __device__ __forceinline__ float exp_f(float x) {
   constexpr float kHi = 1.44269502e+00f, kLo = 1.92596299e-08f;
-  const float t = fmaxf(x, -200.0f);  // (e^-200 is below the least fp32)
-  const float h = t * kHi, l = fmaf(t, kHi, -h) + t * kLo;
-  const float r = __builtin_amdgcn_exp2f(h) * fmaf(l, 0.693147182f, 1.0f);
-  return x != x ? x : r;
+  const float t = __builtin_elementwise_maximum(x, -200.0f);  // (e^-200 is below the least fp32)
+  const float h = t * kHi, l = fmaf(t, kLo, fmaf(t, kHi, -h));
+  return __builtin_amdgcn_exp2f(h) * fmaf(l, 0.693147182f, 1.0f);
 }
 
 }  // namespace mxq
