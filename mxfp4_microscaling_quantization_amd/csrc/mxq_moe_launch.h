@@ -27,8 +27,9 @@ struct SortLaunch {
   int32_t *positions, *order;
   int32_t* counts;  // workspace [blocks, n_experts], then [n_experts]
 };
-// Up to this many assignments one workgroup does everything in one launch.
-constexpr int64_t kSortOne = 4096;
+// Up to this many assignments one workgroup does everything in one launch (256 experts, us: 4096
+// assignments 6.6, 6144 8.5 and 11.4 in three launches, 8192 10.0 and 11.4, 12288 13.4 and 11.4).
+constexpr int64_t kSortOne = 8192;
 // Assignments of a block otherwise: as many as keep the table of counts at 1024 blocks at most.
 constexpr int64_t sort_chunk(int64_t count) {
   return count <= 1024 * 2048 ? 2048 : (count + 1023) / 1024 + 255 & ~(int64_t)255;
