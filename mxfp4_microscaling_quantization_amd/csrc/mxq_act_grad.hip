@@ -33,7 +33,11 @@ __device__ __forceinline__ float act_grad_f(float dy, float z, int act) {
 }
 
 // V elements of a row, as they lie in memory: whole (VEC: every row starts on V elements; data
-// read once, so non-temporal) or one by one, those past the row's end as zeros.
+// read once, so non-temporal), or rows that start on any element (the memory system takes such
+// accesses) with the last elements one by one, those past the row's end as zeros. Stores of 16 bytes of
+// a lane write whole lines and go past the caches; stores of 8 do better through them (65536 x 4096 bf16
+// swiglu from FP8 with h 253 us, past the caches 279), and so do fp32's two pieces of 16, each of which
+// writes half of every line (16384 x 4096 fp32 141 us, past the caches 173).
 template <typename T, int V, bool VEC>
 struct Run {
   T v[V];
@@ -49,23 +53,22 @@ struct Run {
           __builtin_memcpy(v + i * 16 / sizeof(T), &x, 16);
         }
       }
+    } else if (left >= V) {
+      __builtin_memcpy(v, p, sizeof(v));
     } else {
 #pragma unroll
       for (int i = 0; i < V; ++i) v[i] = i < left ? p[i] : (T)0.0f;
     }
   }
   __device__ __forceinline__ void store(T* p, int64_t left) const {
-    if constexpr (VEC && sizeof(v) == 8) {
-      uint2 x;
-      __builtin_memcpy(&x, v, 8);
-      store_nt(reinterpret_cast<uint2*>(p), x);
+    if constexpr (VEC && sizeof(v) == 16) {
+      uint4 x;
+      __builtin_memcpy(&x, v, 16);
+      store_nt(reinterpret_cast<uint4*>(p), x);
     } else if constexpr (VEC) {
-#pragma unroll
-      for (int i = 0; i < (int)sizeof(v) / 16; ++i) {
-        uint4 x;
-        __builtin_memcpy(&x, v + i * 16 / sizeof(T), 16);
-        store_nt(reinterpret_cast<uint4*>(p) + i, x);
-      }
+      __builtin_memcpy(__builtin_assume_aligned(p, sizeof(v) < 16 ? sizeof(v) : 16), v, sizeof(v));
+    } else if (left >= V) {
+      __builtin_memcpy(p, v, sizeof(v));
     } else {
 #pragma unroll
       for (int i = 0; i < V; ++i)
@@ -95,6 +98,8 @@ struct ZRun8 {
     scale = as_u(p.z_scales[row * ((p.n + 127) / 128) + col / 128]);
     if constexpr (VEC) {
       q = load_nt(reinterpret_cast<const uint2*>(z));
+    } else if (left >= 8) {
+      __builtin_memcpy(&q, z, 8);
     } else {
       uint8_t b[8];
 #pragma unroll
@@ -114,10 +119,9 @@ struct ZRun8 {
 // One workgroup: up to p.block_rows rows of one group, 512 columns. Its waves take every
 // fourth row, four of them in flight: their loads go ahead of the first one's arithmetic.
 // The sums of the four waves are added in order through LDS. H: act(z) goes out as well.
-template <typename T, typename Z, bool SUM, bool GATED, bool VEC, bool H>
+template <typename T, typename Z, bool SUM, bool GATED, bool VEC, bool H, int U>
 __device__ __forceinline__ void grad_block(const ActGradLaunch& p, int col_tiles) {
   __shared__ float sums[4][kCols];
-  constexpr int U = 4;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int block = blockIdx.x / col_tiles, col_tile = blockIdx.x % col_tiles;
   Segment s{0, 0, p.rows, block};
@@ -190,12 +194,14 @@ __device__ __forceinline__ void grad_block(const ActGradLaunch& p, int col_tiles
 // plain stream that reads twice what it writes reaches here.
 template <typename T, bool SUM, bool GATED, bool VEC>
 __global__ __launch_bounds__(256) void act_grad_kernel(ActGradLaunch p, int col_tiles) {
-  grad_block<T, ZRun<T, VEC>, SUM, GATED, VEC, false>(p, col_tiles);
+  grad_block<T, ZRun<T, VEC>, SUM, GATED, VEC, false, 4>(p, col_tiles);
 }
 
+// Eight rows of a wave in flight: 65536 x 4096 bf16 swiglu from FP8 with its sums and h, 1.35 GB, 251 us,
+// 5.4 TB/s (four 253; without h 211 and 219). Rows that start anywhere: four (146 and 141 us of 16384 x 4098).
 template <typename T, bool SUM, bool GATED, bool VEC, bool H>
 __global__ __launch_bounds__(256) void fp8_act_grad_kernel(ActGradLaunch p, int col_tiles) {
-  grad_block<T, ZRun8<VEC>, SUM, GATED, VEC, H>(p, col_tiles);
+  grad_block<T, ZRun8<VEC>, SUM, GATED, VEC, H, VEC ? 8 : 4>(p, col_tiles);
 }
 
 // db[g] = the partial sums of the group's row blocks. A column has kLanes threads, each with

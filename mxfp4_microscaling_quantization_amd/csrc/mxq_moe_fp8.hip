@@ -21,7 +21,8 @@ struct Fp8Params {
 };
 
 // A thread takes chunks base + 256 j, so a wave's loads and stores are contiguous and a group is 16
-// neighbouring lanes. VEC: rows of x start on 16 bytes and cols is a multiple of 8.
+// neighbouring lanes. VEC: rows of x start on 16 bytes and cols is a multiple of 8; otherwise rows start
+// anywhere (the memory system takes such accesses), and a row's last elements go one by one.
 template <typename T, bool VEC>
 __global__ __launch_bounds__(kThreads) void fp8_rows_kernel(Fp8Params p) {
   const uint32_t base = blockIdx.x * kChunks + threadIdx.x;
@@ -40,6 +41,8 @@ __global__ __launch_bounds__(kThreads) void fp8_rows_kernel(Fp8Params p) {
     const size_t off = (size_t)(row[u] * p.ldx + col[u]);
     if constexpr (VEC) {
       if (left[u] > 0) load_raw(x, off, raw[u]);
+    } else if (left[u] >= 8) {
+      __builtin_memcpy(&raw[u], x + off, 8 * sizeof(T));
     } else {
       T t[8];
 #pragma unroll
@@ -56,6 +59,8 @@ __global__ __launch_bounds__(kThreads) void fp8_rows_kernel(Fp8Params p) {
     uint8_t* to = p.q8 + row[u] * p.cols + col[u];
     if constexpr (VEC) {
       if (left[u] > 0) *reinterpret_cast<uint2*>(to) = make_uint2(q[0], q[1]);
+    } else if (left[u] >= 8) {
+      __builtin_memcpy(to, q, 8);
     } else {
 #pragma unroll
       for (int i = 0; i < 8; ++i)
