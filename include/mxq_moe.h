@@ -8,6 +8,10 @@
  * the rows of all experts is positions[t, k + j]; a position outside [0, rows) (-1, as
  * mxq_expert_sort writes it) stands for an assignment without a row, which reads and
  * writes nothing. Two assignments must not have the same row.
+ *
+ * Limits: fewer than 2^31 assignments, rows and tokens, 2^40 elements of a matrix, 2^22
+ * columns of a row that is sent or combined (beyond them MXQ_ESHAPE), 4096 experts, 64
+ * choices of a token (MXQ_EINVAL). 0 tokens, or 0 rows to write, are no-ops.
  */
 #ifndef MXQ_MOE_H_
 #define MXQ_MOE_H_

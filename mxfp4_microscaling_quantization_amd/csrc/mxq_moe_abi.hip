@@ -25,8 +25,7 @@ mxq_status check_rows(int64_t tokens, int64_t top_k, int64_t rows, int64_t width
   if (tokens < 0 || rows < 0 || width < 0) return MXQ_EINVAL;
   if (top_k < 1 || top_k > kMaxTopK) return MXQ_EINVAL;
   if (tokens > kMaxDim / top_k || rows > kMaxDim || width == 0 || width > kMaxWidth) return MXQ_ESHAPE;
-  // (a workgroup takes 256 columns of a token at least)
-  if (tokens > kMaxGrid / ((width + 255) / 256)) return MXQ_ESHAPE;
+  if (tokens > ((int64_t)1 << 40) / width || rows > ((int64_t)1 << 40) / width) return MXQ_ESHAPE;
   return MXQ_OK;
 }
 

@@ -6,6 +6,18 @@
 
 namespace mxq {
 
+// launch(first token, tokens) for runs of tokens that one launch holds: grids count threads in 32 bits.
+template <typename F>
+hipError_t by_slabs(int64_t tokens, int64_t threads_of_token, F&& launch) {
+  const int64_t most = ((int64_t)1 << 31) / threads_of_token;
+  for (int64_t t0 = 0; t0 < tokens; t0 += most) {
+    launch(t0, tokens - t0 < most ? tokens - t0 : most);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
+}
+
 struct RouteLaunch {
   const void* logits;  // [tokens, experts], row stride ld
   int f32;

@@ -349,11 +349,22 @@ __global__ __launch_bounds__(256) void route_grad_kernel(RouteLaunch p) {
 }
 
 template <typename T, int G, int V>
-hipError_t launch_g(const RouteLaunch& a, bool grad, hipStream_t st) {
-  const dim3 grid((uint32_t)((a.tokens + 256 / G - 1) / (256 / G)));
-  if (grad) route_grad_kernel<T, G, V><<<grid, 256, 0, st>>>(a);
-  else route_kernel<T, G, V><<<grid, 256, 0, st>>>(a);
-  return hipGetLastError();
+hipError_t launch_g(const RouteLaunch& all, bool grad, hipStream_t st) {
+  return by_slabs(all.tokens, G, [&](int64_t t0, int64_t tokens) {
+    RouteLaunch a = all;
+    a.tokens = tokens;
+    if (a.logits) a.logits = static_cast<const T*>(all.logits) + t0 * all.ld;
+    a.weights += t0 * all.top_k;
+    a.chosen += t0 * all.top_k;
+    const dim3 grid((uint32_t)((tokens + 256 / G - 1) / (256 / G)));
+    if (grad) {
+      a.dw += t0 * all.top_k;
+      a.dlogits = static_cast<T*>(all.dlogits) + t0 * all.experts;
+      route_grad_kernel<T, G, V><<<grid, 256, 0, st>>>(a);
+    } else {
+      route_kernel<T, G, V><<<grid, 256, 0, st>>>(a);
+    }
+  });
 }
 
 // Lanes of a token: few leave more logits to a lane, which then more often gives away its four; many

@@ -288,43 +288,69 @@ __global__ __launch_bounds__(kGradThreads) void combine_grad_kernel(RowsLaunch p
   if (left & 1) grad_rows<G, Y, WHOLE, DW, 1>(p, a, g, parts);
 }
 
+// The launch for tokens t0 to t0 + tokens, with the pointers to the tokens' data moved on; `x` and `out`:
+// bytes of a token there (0 where they are the experts' rows), `res` likewise.
+RowsLaunch slab(const RowsLaunch& all, int64_t t0, int64_t tokens, int64_t x, int64_t res, int64_t out) {
+  RowsLaunch a = all;
+  a.tokens = tokens;
+  a.x = static_cast<const char*>(all.x) + t0 * x;
+  if (all.res) a.res = static_cast<const char*>(all.res) + t0 * res;
+  a.out = static_cast<char*>(all.out) + t0 * out;
+  a.positions += t0 * all.top_k;
+  if (all.weights) a.weights += t0 * all.top_k;
+  if (all.dw) a.dw += t0 * all.top_k;
+  return a;
+}
+
 template <bool WHOLE>
-void launch_copy(const RowsLaunch& a, int64_t ld, int64_t bytes, hipStream_t st) {
+hipError_t launch_copy(const RowsLaunch& all, int64_t ld, int64_t bytes, hipStream_t st) {
   constexpr int kThreads = kCopyThreads<WHOLE>;
   const int tiles = (int)((bytes + kThreads * 16 - 1) / (kThreads * 16));
-  dispatch_copy_kernel<WHOLE><<<dim3((uint32_t)(a.tokens * tiles)), kThreads, 0, st>>>(a, ld, (int)bytes, tiles);
+  return by_slabs(all.tokens, (int64_t)tiles * kThreads, [&](int64_t t0, int64_t tokens) {
+    const RowsLaunch a = slab(all, t0, tokens, ld, 0, 0);
+    dispatch_copy_kernel<WHOLE><<<dim3((uint32_t)(tokens * tiles)), kThreads, 0, st>>>(a, ld, (int)bytes, tiles);
+  });
 }
 
 template <typename T, bool FP8>
-void launch_quantize(const RowsLaunch& a, hipStream_t st) {
-  const int64_t waves = (a.width / (FP8 ? 16 : 32) + 63) / 64;
+hipError_t launch_quantize(const RowsLaunch& all, hipStream_t st) {
+  const int64_t waves = (all.width / (FP8 ? 16 : 32) + 63) / 64;
   // few tokens: a wave for each part
-  const bool few = a.tokens < 1024;
+  const bool few = all.tokens < 1024;
   const int threads = few ? 64 : 64 * (int)(waves < kQuantThreads / 64 ? waves : kQuantThreads / 64);
   const int tiles = few ? (int)waves : 1;
-  dispatch_quantize_kernel<T, FP8><<<dim3((uint32_t)(a.tokens * tiles)), threads, 0, st>>>(a, tiles);
+  return by_slabs(all.tokens, (int64_t)tiles * threads, [&](int64_t t0, int64_t tokens) {
+    const RowsLaunch a = slab(all, t0, tokens, all.ldx * (int64_t)sizeof(T), 0, 0);
+    dispatch_quantize_kernel<T, FP8><<<dim3((uint32_t)(tokens * tiles)), threads, 0, st>>>(a, tiles);
+  });
 }
 
 template <typename Y, typename O>
-void launch_combine_t(const RowsLaunch& a, hipStream_t st) {
-  const int tiles = (int)((a.width + 511) / 512);
-  const dim3 grid((uint32_t)(a.tokens * tiles));
-  if (a.width % 8 == 0) combine_kernel<Y, O, true><<<grid, 64, 0, st>>>(a, tiles);
-  else combine_kernel<Y, O, false><<<grid, 64, 0, st>>>(a, tiles);
+hipError_t launch_combine_t(const RowsLaunch& all, hipStream_t st) {
+  const int tiles = (int)((all.width + 511) / 512);
+  return by_slabs(all.tokens, (int64_t)tiles * 64, [&](int64_t t0, int64_t tokens) {
+    const int64_t row = all.width * (int64_t)sizeof(O);
+    const RowsLaunch a = slab(all, t0, tokens, 0, row, row);
+    const dim3 grid((uint32_t)(tokens * tiles));
+    if (a.width % 8 == 0) combine_kernel<Y, O, true><<<grid, 64, 0, st>>>(a, tiles);
+    else combine_kernel<Y, O, false><<<grid, 64, 0, st>>>(a, tiles);
+  });
 }
 
 template <typename G, typename Y, bool WHOLE>
-void launch_combine_grad_v(const RowsLaunch& a, hipStream_t st) {
-  const int64_t waves = (a.width + 511) / 512;
+hipError_t launch_combine_grad_v(const RowsLaunch& all, hipStream_t st) {
+  const int64_t waves = (all.width + 511) / 512;
   const int threads = 64 * (int)(waves < kGradThreads / 64 ? waves : kGradThreads / 64);
-  const dim3 grid((uint32_t)a.tokens);
-  if (a.dw) combine_grad_kernel<G, Y, WHOLE, true><<<grid, threads, 0, st>>>(a);
-  else combine_grad_kernel<G, Y, WHOLE, false><<<grid, threads, 0, st>>>(a);
+  return by_slabs(all.tokens, threads, [&](int64_t t0, int64_t tokens) {
+    const RowsLaunch a = slab(all, t0, tokens, all.width * (int64_t)sizeof(G), 0, 0);
+    const dim3 grid((uint32_t)tokens);
+    if (a.dw) combine_grad_kernel<G, Y, WHOLE, true><<<grid, threads, 0, st>>>(a);
+    else combine_grad_kernel<G, Y, WHOLE, false><<<grid, threads, 0, st>>>(a);
+  });
 }
 template <typename G, typename Y>
-void launch_combine_grad_t(const RowsLaunch& a, hipStream_t st) {
-  if (a.width % 8 == 0) launch_combine_grad_v<G, Y, true>(a, st);
-  else launch_combine_grad_v<G, Y, false>(a, st);
+hipError_t launch_combine_grad_t(const RowsLaunch& a, hipStream_t st) {
+  return a.width % 8 == 0 ? launch_combine_grad_v<G, Y, true>(a, st) : launch_combine_grad_v<G, Y, false>(a, st);
 }
 
 }  // namespace
@@ -332,25 +358,21 @@ void launch_combine_grad_t(const RowsLaunch& a, hipStream_t st) {
 hipError_t launch_dispatch(const RowsLaunch& a, hipStream_t st) {
   if (a.fmt == 0) {
     const int64_t size = a.x_f32 ? 4 : 2, bytes = a.width * size, ld = a.ldx * size;
-    if (((uint64_t)(uintptr_t)a.x | (uint64_t)(ld | bytes)) % 16 == 0) launch_copy<true>(a, ld, bytes, st);
-    else launch_copy<false>(a, ld, bytes, st);
-  } else {
-    if (a.fmt == 1) a.x_f32 ? launch_quantize<float, false>(a, st) : launch_quantize<uint16_t, false>(a, st);
-    else a.x_f32 ? launch_quantize<float, true>(a, st) : launch_quantize<uint16_t, true>(a, st);
+    const bool whole = ((uint64_t)(uintptr_t)a.x | (uint64_t)(ld | bytes)) % 16 == 0;
+    return whole ? launch_copy<true>(a, ld, bytes, st) : launch_copy<false>(a, ld, bytes, st);
   }
-  return hipGetLastError();
+  if (a.fmt == 1) return a.x_f32 ? launch_quantize<float, false>(a, st) : launch_quantize<uint16_t, false>(a, st);
+  return a.x_f32 ? launch_quantize<float, true>(a, st) : launch_quantize<uint16_t, true>(a, st);
 }
 
 hipError_t launch_combine(const RowsLaunch& a, hipStream_t st) {
-  if (a.x_f32) a.out_f32 ? launch_combine_t<float, float>(a, st) : launch_combine_t<float, __bf16>(a, st);
-  else a.out_f32 ? launch_combine_t<__bf16, float>(a, st) : launch_combine_t<__bf16, __bf16>(a, st);
-  return hipGetLastError();
+  if (a.x_f32) return a.out_f32 ? launch_combine_t<float, float>(a, st) : launch_combine_t<float, __bf16>(a, st);
+  return a.out_f32 ? launch_combine_t<__bf16, float>(a, st) : launch_combine_t<__bf16, __bf16>(a, st);
 }
 
 hipError_t launch_combine_grad(const RowsLaunch& a, hipStream_t st) {
-  if (a.x_f32) a.out_f32 ? launch_combine_grad_t<float, float>(a, st) : launch_combine_grad_t<float, __bf16>(a, st);
-  else a.out_f32 ? launch_combine_grad_t<__bf16, float>(a, st) : launch_combine_grad_t<__bf16, __bf16>(a, st);
-  return hipGetLastError();
+  if (a.x_f32) return a.out_f32 ? launch_combine_grad_t<float, float>(a, st) : launch_combine_grad_t<float, __bf16>(a, st);
+  return a.out_f32 ? launch_combine_grad_t<__bf16, float>(a, st) : launch_combine_grad_t<__bf16, __bf16>(a, st);
 }
 
 }  // namespace mxq

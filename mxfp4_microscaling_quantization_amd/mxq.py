@@ -483,13 +483,15 @@ def mxq_route(logits: torch.Tensor, top_k: int, renorm: bool = False, out=None):
     tokens, n_experts, ld = _strided_rows(logits, "logits")
     dt = _float_code(logits.dtype)
     shape = (tokens, top_k)
-    if out is None:
+    if out is None:  # (what is made here needs no checks: 0.4 us each, where a small call takes 8)
+        stream = _on_gpu(logits)
         out = logits.new_empty(shape, dtype=torch.float32), logits.new_empty(shape, dtype=torch.int32)
-    weights, experts = out
-    wp, ep = _dense(weights, shape, torch.float32, "weights"), _dense(experts, shape, torch.int32, "experts")
-    stream = _on_gpu(logits, weights, experts)
+        wp, ep = out[0].data_ptr(), out[1].data_ptr()
+    else:
+        wp, ep = _dense(out[0], shape, torch.float32, "weights"), _dense(out[1], shape, torch.int32, "experts")
+        stream = _on_gpu(logits, *out)
     _check(lib().mxq_route(logits.data_ptr(), dt, tokens, n_experts, ld, top_k, int(renorm), wp, ep, stream))
-    return weights, experts
+    return out
 
 
 def mxq_route_grad(dw: torch.Tensor, weights: torch.Tensor, experts: torch.Tensor, logits: torch.Tensor,
@@ -503,9 +505,12 @@ def mxq_route_grad(dw: torch.Tensor, weights: torch.Tensor, experts: torch.Tenso
     dwp = _dense(dw, shape, torch.float32, "dw")
     wp, ep = _dense(weights, shape, torch.float32, "weights"), _dense(experts, shape, torch.int32, "experts")
     if out is None:
+        stream = _on_gpu(logits, dw, weights, experts)
         out = logits.new_empty((tokens, n_experts))
-    op = _dense(out, (tokens, n_experts), logits.dtype, "out")
-    stream = _on_gpu(logits, dw, weights, experts, out)
+        op = out.data_ptr()
+    else:
+        op = _dense(out, (tokens, n_experts), logits.dtype, "out")
+        stream = _on_gpu(logits, dw, weights, experts, out)
     _check(lib().mxq_route_grad(dwp, wp, ep, logits.data_ptr(), dt, tokens, n_experts, ld, shape[1], int(renorm), op,
                                 stream))
     return out
@@ -523,18 +528,21 @@ def mxq_expert_sort(experts: torch.Tensor, n_experts: int, out: Optional[ExpertR
     values outside [0, n_experts) have no row), those of one expert in the tokens' order.
     `workspace` (uint8, mxq_expert_sort_workspace bytes) is allocated if absent."""
     ep, count = _dense(experts, experts.shape, torch.int32, "experts"), experts.numel()
+    need = lib().mxq_expert_sort_workspace(count, n_experts)
+    if workspace is not None and (workspace.numel() * workspace.element_size() < need or not workspace.is_contiguous()):
+        raise ValueError(f"dense workspace of {need} bytes expected")
     if out is None:
+        stream = _on_gpu(experts, workspace)
         out = ExpertRows(experts.new_empty((n_experts + 1,), dtype=torch.int64), torch.empty_like(experts),
                          experts.new_empty((count,)))
-    offsets, positions, order = out
-    offp = _dense(offsets, (n_experts + 1,), torch.int64, "offsets")
-    pp, op = _dense(positions, experts.shape, torch.int32, "positions"), _dense(order, (count,), torch.int32, "order")
-    need = lib().mxq_expert_sort_workspace(count, n_experts)
-    if workspace is None:
-        workspace = experts.new_empty((need,), dtype=torch.uint8) if need else None
-    elif workspace.numel() * workspace.element_size() < need or not workspace.is_contiguous():
-        raise ValueError(f"dense workspace of {need} bytes expected")
-    stream = _on_gpu(experts, offsets, positions, order, workspace)
+        offp, pp, op = out[0].data_ptr(), out[1].data_ptr(), out[2].data_ptr()
+    else:
+        offp = _dense(out[0], (n_experts + 1,), torch.int64, "offsets")
+        pp = _dense(out[1], experts.shape, torch.int32, "positions")
+        op = _dense(out[2], (count,), torch.int32, "order")
+        stream = _on_gpu(experts, *out, workspace)
+    if need and workspace is None:
+        workspace = experts.new_empty((need,), dtype=torch.uint8)
     _check(lib().mxq_expert_sort(ep, count, n_experts, offp, pp, op, _ptr(workspace), stream))
     return out
 
@@ -552,18 +560,26 @@ def mxq_dispatch(x: torch.Tensor, positions: torch.Tensor, rows: Optional[int] =
         raise ValueError(f"positions of {positions.shape[0]} tokens for {tokens}")
     if rows is None:
         rows = positions.numel() if out is None else (out if code == 0 else out[0]).shape[0]
+    sp = None
     if code == 0:
         if out is None:
+            stream = _on_gpu(x, positions)
             out = x.new_empty((rows, width))
-        op, sp, given = _dense(out, (rows, width), x.dtype, "out"), None, (out,)
+            op = out.data_ptr()
+        else:
+            op = _dense(out, (rows, width), x.dtype, "out")
+            stream = _on_gpu(x, positions, out)
     else:
         per, block, kind = (2, 32, torch.uint8) if code == 1 else (1, 128, torch.float32)
         if out is None:
+            stream = _on_gpu(x, positions)
             out = (x.new_empty((rows, width // per), dtype=torch.uint8),
                    x.new_empty((rows, width // block), dtype=kind))
-        op = _dense(out[0], (rows, width // per), torch.uint8, "codes")
-        sp, given = _dense(out[1], (rows, width // block), kind, "scales"), out
-    stream = _on_gpu(x, positions, *given)
+            op, sp = out[0].data_ptr(), out[1].data_ptr()
+        else:
+            op = _dense(out[0], (rows, width // per), torch.uint8, "codes")
+            sp = _dense(out[1], (rows, width // block), kind, "scales")
+            stream = _on_gpu(x, positions, *out)
     _check(lib().mxq_dispatch(x.data_ptr(), dt, tokens, width, ldx, positions.data_ptr(), positions.shape[1], rows,
                               code, op, sp, stream))
     return out
@@ -584,9 +600,12 @@ def mxq_combine(y: torch.Tensor, positions: torch.Tensor, weights: Optional[torc
     wp = None if weights is None else _dense(weights, shape, torch.float32, "weights")
     rp = None if residual is None else _dense(residual, (tokens, width), out_dtype, "residual")
     if out is None:
+        stream = _on_gpu(y, positions, weights, residual)
         out = y.new_empty((tokens, width), dtype=out_dtype)
-    op = _dense(out, (tokens, width), out_dtype, "out")
-    stream = _on_gpu(y, positions, weights, residual, out)
+        op = out.data_ptr()
+    else:
+        op = _dense(out, (tokens, width), out_dtype, "out")
+        stream = _on_gpu(y, positions, weights, residual, out)
     _check(lib().mxq_combine(yp, ydt, rows, width, positions.data_ptr(), wp, tokens, shape[1], rp, op, dt, stream))
     return out
 
@@ -623,9 +642,13 @@ def mxq_fp8_quantize(x: torch.Tensor, out=None):
     rows, cols, ldx = _strided_rows(x, "x")
     dt, groups = _float_code(x.dtype), (cols + 127) // 128
     if out is None:
+        stream = _on_gpu(x)
         out = x.new_empty((rows, cols), dtype=torch.uint8), x.new_empty((rows, groups), dtype=torch.float32)
-    qp, sp = _dense(out[0], (rows, cols), torch.uint8, "codes"), _dense(out[1], (rows, groups), torch.float32, "scales")
-    stream = _on_gpu(x, *out)
+        qp, sp = out[0].data_ptr(), out[1].data_ptr()
+    else:
+        qp = _dense(out[0], (rows, cols), torch.uint8, "codes")
+        sp = _dense(out[1], (rows, groups), torch.float32, "scales")
+        stream = _on_gpu(x, *out)
     _check(lib().mxq_fp8_quantize(x.data_ptr(), dt, rows, cols, ldx, qp, sp, stream))
     return out
 

@@ -38,9 +38,13 @@ def check_copy(tokens, k, width, dtype, extra=0, first=0, missing=0.2, spare=5, 
     assert np.array_equal(bits(got).cpu().numpy(), want)
 
 
+COPIES = [(1, 1, 1), (1, 8, 8), (3, 2, 7), (5, 3, 130), (2, 64, 24), (7, 5, 2056), (4, 2, 4100), (2100, 2, 264),
+          (2100, 3, 33)]
+QUANTISED = [(1, 1, 128), (3, 2, 384), (6, 8, 2176), (5, 2, 4096), (2, 1, 16512), (1060, 2, 256), (1030, 1, 9216)]
+
+
 @pytest.mark.parametrize("dtype", DTYPES)
-@pytest.mark.parametrize("tokens,k,width", [(1, 1, 1), (1, 8, 8), (3, 2, 7), (5, 3, 130), (2, 64, 24), (7, 5, 2056),
-                                            (4, 2, 4100), (2100, 2, 264), (2100, 3, 33)])
+@pytest.mark.parametrize("tokens,k,width", COPIES)
 def test_copy(tokens, k, width, dtype):
     require_gpu()
     check_copy(tokens, k, width, dtype)
@@ -55,7 +59,7 @@ def test_copy_strides(dtype):
 
 @pytest.mark.parametrize("dtype", DTYPES)
 @pytest.mark.parametrize("fmt", ["mxfp4", "fp8"])
-@pytest.mark.parametrize("tokens,k,width", [(1, 1, 128), (3, 2, 384), (6, 8, 2176), (5, 2, 4096), (2060, 2, 256)])
+@pytest.mark.parametrize("tokens,k,width", QUANTISED)
 def test_quantised(tokens, k, width, fmt, dtype):
     """The bits of the row quantisers on the token's row, in the rows of its assignments only."""
     require_gpu()

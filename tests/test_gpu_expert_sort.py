@@ -33,16 +33,19 @@ def check(e: np.ndarray, n: int):
     assert r.positions.shape == e.shape
 
 
-@pytest.mark.parametrize("n", [1, 2, 64, 512, 513, 4096])
-@pytest.mark.parametrize("tokens,k", [(1, 1), (1, 8), (8, 8), (37, 3), (64, 1), (1365, 3), (4097, 1), (4096, 2)])
+ONE = [(tokens, k, n) for tokens, k in ((1, 1), (1, 8), (8, 8), (37, 3), (64, 1), (1365, 3), (4097, 1), (4096, 2))
+       for n in (1, 2, 64, 512, 513, 4096)]
+MANY = [(count, n) for count in (8193, 10007, 70001) for n in (1, 3, 65, 256, 1024, 1025, 4096)]
+
+
+@pytest.mark.parametrize("tokens,k,n", ONE)
 def test_one_workgroup(tokens, k, n):
     require_gpu()
     rng = np.random.default_rng(n + tokens)
     check(choices(rng, tokens, n, min(k, n), 0.1), n)
 
 
-@pytest.mark.parametrize("n", [1, 3, 65, 256, 2048, 2049, 4096])
-@pytest.mark.parametrize("count", [8193, 10007, 70001])
+@pytest.mark.parametrize("count,n", MANY)
 def test_many_workgroups(count, n):
     require_gpu()
     rng = np.random.default_rng(n + count)

@@ -20,9 +20,11 @@ def check(x: torch.Tensor, of: torch.Tensor = None):
     assert_equal_bits(u8(q), wq, "codes")
 
 
+SIZES = [(1, 1), (3, 7), (2, 8), (5, 127), (4, 128), (4, 129), (9, 136), (3, 1336), (70, 4104), (300, 1024), (2, 8193)]
+
+
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
-@pytest.mark.parametrize("rows,cols", [(1, 1), (3, 7), (2, 8), (5, 127), (4, 128), (4, 129), (9, 136), (3, 1336),
-                                       (70, 4104), (300, 1024), (2, 8193)])
+@pytest.mark.parametrize("rows,cols", SIZES)
 def test_sizes(rows, cols, dtype):
     require_gpu()
     rng = np.random.default_rng(rows + cols)
