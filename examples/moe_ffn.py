@@ -1,12 +1,14 @@
 """A mixture-of-experts FFN layer trained through libmxq's matrix products, end to end:
 
-  forward   route, sort the tokens by expert, quantise them to MXFP4,
+  forward   choose the experts, sort the tokens by expert, send them there in MXFP4,
             [z, h] = swiglu(x W1^T + b1) per expert, quantise h, y = h W2^T + b2, combine
-  backward  quantise dy, dh = dy W2, dz = act'(z) dh with db1, quantise dz, dx = dz W1,
+  backward  dy and the router's gradient from the combined result's, quantise dy, dh = dy W2,
+            dz = act'(z) dh with db1, quantise dz, dx = dz W1 (combined without weights),
             dW1 and dW2 from the FP8 columns of the quantised tokens
 
 Weights are quantised once, row-wise for the forward products and column-wise for the
-input gradients. W1's rows are gate/up pairs: row 2j is gate j, row 2j + 1 up j.
+input gradients. W1's rows are gate/up pairs: row 2j is gate j, row 2j + 1 up j. z is kept for
+the backward pass in bf16, or in FP8 (keep="fp8"), from which h is formed again.
 
 Usage: python -m examples.moe_ffn [tokens hidden ffn experts top_k]
 """
@@ -33,12 +35,28 @@ class Weights(NamedTuple):
 
 
 class Saved(NamedTuple):
-    order: torch.Tensor       # the token of every routed row
-    weight: torch.Tensor      # its routing weight [R, 1]
-    offsets: torch.Tensor     # int64 [E + 1], rows of every expert
+    logits: torch.Tensor
+    weights: torch.Tensor     # routing weights [T, k]
+    experts: torch.Tensor
+    rows: mxq.ExpertRows
     xq: mxq.Quantized
-    z: torch.Tensor
-    hq: mxq.Quantized
+    z: object                 # bf16 [R, 2F], or FP8 (codes, scales)
+    hq: object                # quantised h; None where it is formed again
+    y: torch.Tensor           # the experts' results [R, H]
+
+    @property
+    def offsets(self) -> torch.Tensor:
+        return self.rows.offsets
+
+    @property
+    def order(self) -> torch.Tensor:
+        """The token of every routed row."""
+        return self.rows.order.long() // self.weights.shape[1]
+
+    @property
+    def weight(self) -> torch.Tensor:
+        """Its routing weight [R, 1]."""
+        return self.weights.flatten()[self.rows.order.long(), None]
 
 
 def quantise_weights(w1, w2, b1, b2) -> Weights:
@@ -52,48 +70,48 @@ def quantise_weights(w1, w2, b1, b2) -> Weights:
     return Weights(w1, w2, b1, b2, w1_rows, w2_rows, w1_cols, w2_cols)
 
 
-def route(logits: torch.Tensor, top_k: int):
-    """Top-k routing: (token of every routed row, its weight, offsets of the experts' rows)."""
-    weight, expert = logits.softmax(-1).topk(top_k, dim=-1)
-    by_expert = expert.flatten().argsort(stable=True)
-    counts = torch.bincount(expert.flatten(), minlength=logits.shape[1])
-    offsets = torch.cat([counts.new_zeros(1), counts.cumsum(0)])
-    return by_expert // top_k, weight.flatten()[by_expert, None], offsets
-
-
 def rows(q: mxq.Quantized):
     return q.codes_row, q.scales_row
 
 
-def forward(x: torch.Tensor, logits: torch.Tensor, w: Weights, top_k: int):
-    """(output [T, H] fp32, what the backward pass needs)."""
-    order, weight, offsets = route(logits, top_k)
-    xq = mxq.mxq_quantize(x[order])
-    h, z = mxq.mxq_grouped_gemm(rows(xq), w.w1_rows, offsets, bias=w.b1, act="swiglu", preact=True)
+def forward(x: torch.Tensor, logits: torch.Tensor, w: Weights, top_k: int, keep: str = "bf16"):
+    """(output [T, H] fp32, what the backward pass needs); keep: how z waits for it, "bf16" or "fp8"."""
+    weights, experts = mxq.mxq_route(logits, top_k)
+    r = mxq.mxq_expert_sort(experts, logits.shape[1])
+    xq = mxq.Quantized(*mxq.mxq_dispatch(x, r.positions, fmt="mxfp4"), None, None, None)
+    h, z = mxq.mxq_grouped_gemm(rows(xq), w.w1_rows, r.offsets, bias=w.b1, act="swiglu", preact=True)
     hq = mxq.mxq_quantize(h)
-    y = mxq.mxq_grouped_gemm(rows(hq), w.w2_rows, offsets, bias=w.b2)
-    out = torch.zeros(x.shape, device=x.device)
-    out.index_add_(0, order, weight * y)
-    return out, Saved(order, weight, offsets, xq, z, hq)
+    y = mxq.mxq_grouped_gemm(rows(hq), w.w2_rows, r.offsets, bias=w.b2)
+    out = mxq.mxq_combine(y, r.positions, weights, out_dtype=torch.float32)
+    if keep == "fp8":
+        z, hq = mxq.mxq_fp8_quantize(z), None
+    return out, Saved(logits, weights, experts, r, xq, z, hq, y)
 
 
-def backward(grad: torch.Tensor, s: Saved, w: Weights):
-    """Gradients (dx, dW1, db1, dW2, db2) of a loss with gradient `grad` [T, H] at the output."""
-    dy = (s.weight * grad[s.order]).bfloat16()
+def backward(grad: torch.Tensor, s: Saved, w: Weights, router: bool = False):
+    """Gradients (dx, dW1, db1, dW2, db2) of a loss with gradient `grad` [T, H] at the output, with
+    `router` also that of the logits. What was saved is overwritten."""
+    off, pos = s.rows.offsets, s.rows.positions
+    dy, dweights = mxq.mxq_combine_grad(grad, s.y, pos, s.weights, out=s.y)
     total = dy.shape[0]
     # (act "none" hands dy through; its column sums per expert are the bias gradient)
-    _, db2 = mxq.mxq_act_grad(dy, dy, "none", s.offsets, bias_grad=True)
+    _, db2 = mxq.mxq_act_grad(dy, dy, "none", off, bias_grad=True)
     dyq = mxq.mxq_quantize(dy)
-    dh = mxq.mxq_grouped_gemm(rows(dyq), w.w2_cols, s.offsets)
-    dz, db1 = mxq.mxq_act_grad(dh, s.z, "swiglu", s.offsets, bias_grad=True, out=s.z)
+    dh = mxq.mxq_grouped_gemm(rows(dyq), w.w2_cols, off)
+    if s.hq is None:
+        dz, db1, h = mxq.mxq_fp8_act_grad(dh, s.z, "swiglu", off, bias_grad=True, recompute=True)
+        hq = mxq.mxq_quantize(h)
+    else:
+        dz, db1 = mxq.mxq_act_grad(dh, s.z, "swiglu", off, bias_grad=True, out=s.z)
+        hq = s.hq
     dzq = mxq.mxq_quantize(dz)
-    dx_rows = mxq.mxq_grouped_gemm(rows(dzq), w.w1_cols, s.offsets)
-    cols = [mxq.mxq_fp4_row_to_fp8_col(*rows(q), s.offsets) for q in (dzq, s.xq, dyq, s.hq)]
-    dw1 = mxq.mxq_grouped_wgrad(cols[0], cols[1], s.offsets, total, out_dtype=torch.float32)
-    dw2 = mxq.mxq_grouped_wgrad(cols[2], cols[3], s.offsets, total, out_dtype=torch.float32)
-    dx = torch.zeros(grad.shape, device=grad.device)
-    dx.index_add_(0, s.order, dx_rows.float())
-    return dx, dw1, db1, dw2, db2
+    dx_rows = mxq.mxq_grouped_gemm(rows(dzq), w.w1_cols, off)
+    cols = [mxq.mxq_fp4_row_to_fp8_col(*rows(q), off) for q in (dzq, s.xq, dyq, hq)]
+    dw1 = mxq.mxq_grouped_wgrad(cols[0], cols[1], off, total, out_dtype=torch.float32)
+    dw2 = mxq.mxq_grouped_wgrad(cols[2], cols[3], off, total, out_dtype=torch.float32)
+    dx = mxq.mxq_combine(dx_rows, pos, out_dtype=torch.float32)
+    grads = dx, dw1, db1, dw2, db2
+    return (*grads, mxq.mxq_route_grad(dweights, s.weights, s.experts, s.logits)) if router else grads
 
 
 def make(tokens: int, hidden: int, ffn: int, experts: int, seed: int = 0, device: str = "cuda"):
@@ -110,10 +128,15 @@ def make(tokens: int, hidden: int, ffn: int, experts: int, seed: int = 0, device
 
 
 def reference(x, logits, w: Weights, top_k: int, grad):
-    """The layer and its gradients in fp32 with autograd, from the weights before quantisation."""
-    p = [t.float().requires_grad_() for t in (x, w.w1, w.b1, w.w2, w.b2)]
-    xr, w1, b1, w2, b2 = p
-    order, weight, offsets = route(logits, top_k)
+    """The layer and its gradients (as backward's with `router`) in fp32 with autograd, from the weights
+    before quantisation."""
+    p = [t.float().detach().clone().requires_grad_() for t in (x, w.w1, w.b1, w.w2, w.b2, logits)]
+    xr, w1, b1, w2, b2, l = p
+    weight, expert = l.softmax(-1).topk(top_k, dim=-1)
+    by_expert = expert.flatten().argsort(stable=True)
+    counts = torch.bincount(expert.flatten(), minlength=logits.shape[1])
+    offsets = torch.cat([counts.new_zeros(1), counts.cumsum(0)])
+    order, weight = by_expert // top_k, weight.flatten()[by_expert, None]
     out = torch.zeros(x.shape, device=x.device)
     for e in range(logits.shape[1]):
         r = slice(int(offsets[e]), int(offsets[e + 1]))
@@ -127,19 +150,21 @@ def reference(x, logits, w: Weights, top_k: int, grad):
 def main(tokens=4096, hidden=2048, ffn=1024, experts=16, top_k=2):
     x, logits, w = make(tokens, hidden, ffn, experts)
     grad = torch.randn(tokens, hidden, device=x.device) / tokens
-    for _ in range(3):
-        torch.cuda.synchronize()
-        t = time.perf_counter()
-        out, saved = forward(x, logits, w, top_k)
-        grads = backward(grad, saved, w)
-        torch.cuda.synchronize()
-        t = time.perf_counter() - t
-    flops = 3 * 2 * tokens * top_k * 3 * hidden * ffn
-    print(f"forward and backward of {tokens} tokens, top {top_k} of {experts} experts, {hidden} x {ffn}: "
-          f"{t * 1e3:.2f} ms, {flops / t / 1e12:.0f} TFLOP/s")
-    ref, ref_grads = reference(x, logits, w, top_k, grad)
-    for name, a, b in zip(("output", "dx", "dW1", "db1", "dW2", "db2"), (out, *grads), (ref, *ref_grads)):
-        print(f"  {name}: relative difference from fp32 {float((a - b).norm() / b.norm()):.3f}")
+    for keep in ("bf16", "fp8"):
+        for _ in range(3):
+            torch.cuda.synchronize()
+            t = time.perf_counter()
+            out, saved = forward(x, logits, w, top_k, keep)
+            grads = backward(grad, saved, w, router=True)
+            torch.cuda.synchronize()
+            t = time.perf_counter() - t
+        flops = 3 * 2 * tokens * top_k * 3 * hidden * ffn
+        print(f"forward and backward of {tokens} tokens, top {top_k} of {experts} experts, {hidden} x {ffn}, z kept in "
+              f"{keep}: {t * 1e3:.2f} ms, {flops / t / 1e12:.0f} TFLOP/s")
+        ref, ref_grads = reference(x, logits, w, top_k, grad)
+        for name, a, b in zip(("output", "dx", "dW1", "db1", "dW2", "db2", "dlogits"), (out, *grads),
+                              (ref, *ref_grads)):
+            print(f"  {name}: relative difference from fp32 {float((a - b).norm() / b.norm()):.3f}")
 
 
 if __name__ == "__main__":
