@@ -34,10 +34,10 @@ __device__ __forceinline__ float act_grad_f(float dy, float z, int act) {
 
 // V elements of a row, as they lie in memory: whole (VEC: every row starts on V elements; data
 // read once, so non-temporal), or rows that start on any element (the memory system takes such
-// accesses) with the last elements one by one, those past the row's end as zeros. Stores of 16 bytes of
-// a lane write whole lines and go past the caches; stores of 8 do better through them (65536 x 4096 bf16
-// swiglu from FP8 with h 253 us, past the caches 279), and so do fp32's two pieces of 16, each of which
-// writes half of every line (16384 x 4096 fp32 141 us, past the caches 173).
+// accesses) with the last elements one by one, those past the row's end as zeros. Stores of 16 and 8
+// bytes of a lane write whole lines and go past the caches (65536 x 4096 bf16 swiglu from FP8 with h 269
+// us, through them 280); fp32's two pieces of 16, each of which writes half of every line, do not (16384
+// x 4096 fp32 141 us, past the caches 155).
 template <typename T, int V, bool VEC>
 struct Run {
   T v[V];
@@ -65,6 +65,10 @@ struct Run {
       uint4 x;
       __builtin_memcpy(&x, v, 16);
       store_nt(reinterpret_cast<uint4*>(p), x);
+    } else if constexpr (VEC && sizeof(v) == 8) {
+      uint2 x;
+      __builtin_memcpy(&x, v, 8);
+      store_nt(reinterpret_cast<uint2*>(p), x);
     } else if constexpr (VEC) {
       __builtin_memcpy(__builtin_assume_aligned(p, sizeof(v) < 16 ? sizeof(v) : 16), v, sizeof(v));
     } else if (left >= V) {
@@ -197,8 +201,9 @@ __global__ __launch_bounds__(256) void act_grad_kernel(ActGradLaunch p, int col_
   grad_block<T, ZRun<T, VEC>, SUM, GATED, VEC, false, 4>(p, col_tiles);
 }
 
-// Eight rows of a wave in flight: 65536 x 4096 bf16 swiglu from FP8 with its sums and h, 1.35 GB, 251 us,
-// 5.4 TB/s (four 253; without h 211 and 219). Rows that start anywhere: four (146 and 141 us of 16384 x 4098).
+// Eight rows of a wave in flight: 65536 x 4096 bf16 swiglu from FP8 with its sums and h, 1.35 GB, 269 us,
+// 5.0 TB/s (without h, 1.08 GB, 208; four rows 219). Rows that start anywhere: four (145 and 141 us of
+// 16384 x 4098).
 template <typename T, bool SUM, bool GATED, bool VEC, bool H>
 __global__ __launch_bounds__(256) void fp8_act_grad_kernel(ActGradLaunch p, int col_tiles) {
   grad_block<T, ZRun8<VEC>, SUM, GATED, VEC, H, VEC ? 8 : 4>(p, col_tiles);

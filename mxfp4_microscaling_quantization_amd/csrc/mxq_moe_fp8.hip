@@ -22,7 +22,9 @@ struct Fp8Params {
 
 // A thread takes chunks base + 256 j, so a wave's loads and stores are contiguous and a group is 16
 // neighbouring lanes. VEC: rows of x start on 16 bytes and cols is a multiple of 8; otherwise rows start
-// anywhere (the memory system takes such accesses), and a row's last elements go one by one.
+// anywhere (the memory system takes such accesses), and a row's last elements go one by one. Bound by
+// memory: 65536 x 4096 bf16, 0.81 GB, 127 us, 6.4 TB/s (codes through the caches 136, 16 elements of a
+// thread 133); 16384 x 4098 39 us, by elements 117.
 template <typename T, bool VEC>
 __global__ __launch_bounds__(kThreads) void fp8_rows_kernel(Fp8Params p) {
   const uint32_t base = blockIdx.x * kChunks + threadIdx.x;
@@ -58,7 +60,7 @@ __global__ __launch_bounds__(kThreads) void fp8_rows_kernel(Fp8Params p) {
     fp8_encode<8, 16>(v, q, scale);
     uint8_t* to = p.q8 + row[u] * p.cols + col[u];
     if constexpr (VEC) {
-      if (left[u] > 0) *reinterpret_cast<uint2*>(to) = make_uint2(q[0], q[1]);
+      if (left[u] > 0) store_nt(reinterpret_cast<uint2*>(to), make_uint2(q[0], q[1]));
     } else if (left[u] >= 8) {
       __builtin_memcpy(to, q, 8);
     } else {

@@ -21,9 +21,9 @@ __device__ __forceinline__ int row_at(const RowsLaunch& p, int64_t a) {
 typedef nt_u32x4 any_u32x4 __attribute__((aligned(2)));
 
 // Rows as they are, 16 bytes of a thread. WHOLE: rows start on 16 bytes and hold whole 16s; otherwise
-// they start anywhere, and a row's last bytes go two by two. Loads go past the caches, stores do not: a
-// row's lines are not always written whole by one workgroup. (16384 tokens' 8 rows of 7168 bf16, 2.1 GB:
-// 403 us, 5.2 TB/s, stores past the caches 404 to 455; 2 rows of 4097 bf16: 66 us, element by element 145.)
+// they start anywhere, and a row's last bytes go two by two. (16384 tokens' 8 rows of 7168 bf16, 2.1 GB:
+// 395 us, 5.3 TB/s, with 256 threads 454; 2 rows of 4097 bf16, 0.4 GB: 82 us, with 128 threads 91, stores
+// through the caches 87, element by element 146.)
 template <bool WHOLE>
 constexpr int kCopyThreads = WHOLE ? 128 : 256;
 template <bool WHOLE>
@@ -48,9 +48,9 @@ __global__ __launch_bounds__(kCopyThreads<WHOLE>) void dispatch_copy_kernel(Rows
     if (r < 0) continue;
     char* out = static_cast<char*>(p.out) + (int64_t)r * bytes + c;
     if (WHOLE) {
-      *reinterpret_cast<nt_u32x4*>(out) = v;
+      __builtin_nontemporal_store(v, reinterpret_cast<nt_u32x4*>(out));
     } else if (pairs >= 8) {
-      *reinterpret_cast<any_u32x4*>(out) = v;
+      __builtin_nontemporal_store((any_u32x4)v, reinterpret_cast<any_u32x4*>(out));
     } else {
 #pragma unroll
       for (int i = 0; i < 7; ++i)
@@ -102,8 +102,8 @@ __device__ __forceinline__ uint4 mx_encode32(const uint4 (&w)[8], uint32_t& byte
 // Rows as MXFP4 or FP8, encoded once and stored for every assignment, 16 bytes of codes of a thread: a
 // block of 32 for MXFP4, 16 elements of a group of 128 for FP8. A workgroup takes a whole token, so that
 // the lines of scales, which no store fills, are put together in one L2. (16384 tokens' 8 rows of 7168
-// bf16 in MXFP4, 0.73 GB: 138 us, 5.3 TB/s; a workgroup for each part of a token 141 to 149; 8 elements
-// of a thread 211. FP8, 1.2 GB: 223 us, and 291.)
+// bf16 in MXFP4, 0.73 GB: 136 to 145 us, 5 to 5.4 TB/s; waves for each part of a token 159, codes through
+// the caches 154, 8 elements of a thread 211. FP8, 1.2 GB: 217 to 232 us; 248, and 291.)
 constexpr int kQuantThreads = 256;
 template <typename T, bool FP8>
 __global__ __launch_bounds__(kQuantThreads) void dispatch_quantize_kernel(RowsLaunch p, int tiles) {
@@ -191,8 +191,8 @@ __device__ __forceinline__ void add_rows(const RowsLaunch& p, int64_t first, int
 }
 
 // A wave: 512 columns of a token. (16384 tokens, 8 rows of 7168 bf16 each to fp32, 2.3 GB: 393 us, 5.9
-// TB/s; a workgroup for a whole token, row after row, 474, eight rows in flight 450 to 475, by waves 438,
-// past the caches as here 391. 4097 columns in pieces of 16 bytes that start anywhere 152, by elements 397.)
+// TB/s; a workgroup for a whole token, row after row, 474; stores through the caches 420. 4 rows of 4097
+// columns to bf16 in pieces of 16 bytes that start anywhere 147, by elements 397.)
 template <typename Y, typename O, bool WHOLE>
 __global__ __launch_bounds__(64) void combine_kernel(RowsLaunch p, int tiles) {
   const int64_t token = blockIdx.x / tiles;
