@@ -46,8 +46,16 @@ constexpr int64_t kSortOne = 8192;
 constexpr int64_t sort_chunk(int64_t count) {
   return count <= 1024 * 2048 ? 2048 : (count + 1023) / 1024 + 255 & ~(int64_t)255;
 }
+constexpr int64_t sort_blocks(int64_t count) { return (count + sort_chunk(count) - 1) / sort_chunk(count); }
+// Two launches, every block summing up the table of counts for itself, while all of them together read
+// up to 64 MiB of it; else three. (Two and three launches, us of the kernels: 33600 assignments to 256
+// experts 10.2 and 11.6, 131072 10.1 and 12.0, 524288 14.5 and 13.8, but with the launches' own time
+// 14.7 and 16.6; 524288 to 64 experts 10.7 and 12.2, to 512 19.5 and 15.1.)
+constexpr bool sort_in_two(int64_t count, int64_t experts) {
+  return experts <= 512 && sort_blocks(count) * sort_blocks(count) * experts <= (int64_t)1 << 24;
+}
 constexpr int64_t sort_workspace(int64_t count, int64_t experts) {
-  return count <= kSortOne ? 0 : ((count + sort_chunk(count) - 1) / sort_chunk(count) + 1) * experts * 4;
+  return count <= kSortOne ? 0 : (sort_blocks(count) + 1) * experts * 4;
 }
 hipError_t launch_expert_sort(const SortLaunch& a, hipStream_t st);
 

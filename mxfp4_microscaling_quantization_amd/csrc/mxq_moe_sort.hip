@@ -1,9 +1,10 @@
 // The rows of every expert: a stable counting sort of the assignments by expert.
 //
-// Three launches, joined by a table of counts [blocks, experts]: every block counts the
-// experts of its assignments; a thread per expert turns a part of its column into sums over
-// the blocks before and leaves the total; every block then numbers its assignments. Up to
-// kSortOne assignments a single workgroup does all of it.
+// Launches joined by a table of counts [blocks, experts]: every block counts the experts of its
+// assignments; every block numbers its assignments from the sums of the counts. The sums are
+// formed by each block for itself while the table is small, else by a launch between, in which a
+// thread per expert turns a part of its column into sums over the blocks before and leaves the
+// total. Up to kSortOne assignments a single workgroup does all of it.
 //
 // Numbers inside a block: a wave owns a contiguous part, with a counter per expert in LDS that
 // starts at the expert's rows before that part. Of 64 assignments at a time, each finds the
@@ -11,9 +12,8 @@
 // number of such lanes below itself, and the last of them moves the counter on. No order
 // depends on timing: the only atomics add whole numbers.
 //
-// Bound by latency: 524288 assignments to 256 experts move 6.3 MB and take 13.8 us, 3.5 of them the
-// counting, 3.6 the sums, 7.5 the numbering (23 us with a quarter of the loads in flight and half
-// of the waves).
+// Bound by latency: 524288 assignments to 256 experts move 6.3 MB and take 14.5 us, 3.5 of them the
+// counting (three launches with a quarter of the loads in flight and half of the waves took 23).
 #include "mxq_moe.h"
 
 namespace mxq {
@@ -195,8 +195,9 @@ __global__ __launch_bounds__(64 * kScanWaves) void sort_scan_kernel(SortLaunch p
   __shared__ int part[kScanWaves][64];
   const int n = p.n_experts, wave = threadIdx.x >> 6, e = blockIdx.x * 64 + lane_id();
   const int each = (blocks + kScanWaves - 1) / kScanWaves;
-  const int first = wave * each, last = first + each < blocks ? first + each : blocks;
-  int* column = p.counts + (e < n ? e : 0);
+  const int first = wave * each;
+  const int last = e >= n ? first : first + each < blocks ? first + each : blocks;  // (no blocks behind the last expert)
+  int* column = p.counts + e;
   int held[kHeld], sum = 0;
 #pragma unroll
   for (int i = 0; i < kHeld; ++i) held[i] = first + i < last ? column[(int64_t)(first + i) * n] : 0;
@@ -224,27 +225,57 @@ __global__ __launch_bounds__(64 * kScanWaves) void sort_scan_kernel(SortLaunch p
   if (wave == kScanWaves - 1) column[(int64_t)blocks * n] = before;
 }
 
-template <int W>
+// What a block needs of the counts: table[e], all assignments of expert e, and base[e], those of the
+// blocks before it, summed up by the block itself. The threads share out the rows of every expert.
+template <int THREADS>
+__device__ __forceinline__ void sum_counts(const SortLaunch& p, int blocks, int* table, int* base) {
+  const int n = p.n_experts, parts = THREADS / n, part = threadIdx.x / n, e = threadIdx.x % n;
+  for (int i = threadIdx.x; i < 2 * n; i += THREADS) table[i] = 0;  // (base lies behind table)
+  __syncthreads();
+  if (part < parts) {
+    const int each = (blocks + parts - 1) / parts, first = part * each;
+    const int last = first + each < blocks ? first + each : blocks;
+    int all = 0, before = 0;
+#pragma unroll 16
+    for (int b = first; b < last; ++b) {
+      const int c = p.counts[(int64_t)b * n + e];
+      all += c;
+      before += b < (int)blockIdx.x ? c : 0;
+    }
+    atomicAdd(&table[e], all);
+    atomicAdd(&base[e], before);
+  }
+}
+
+// SUM: the counts are as sort_count_kernel left them; otherwise as sort_scan_kernel did.
+template <int W, bool SUM>
 __global__ __launch_bounds__(64 * W) void sort_number_kernel(SortLaunch p, int64_t chunk, int blocks) {
-  extern __shared__ int lds[];  // counters [W][n_experts], table [n_experts + 1]
+  extern __shared__ int lds[];  // counters [W][n_experts], SUM: table and base [n_experts] each, else table [n_experts]
+  __shared__ int rows;
   const int n = p.n_experts;
   int* table = lds + W * n;
   const int* mine = p.counts + (int64_t)blockIdx.x * n;
-  int held = threadIdx.x < n ? mine[threadIdx.x] : 0;  // (asked for early: most calls have no more experts than threads)
-  for (int i = threadIdx.x; i < n; i += 64 * W) table[i] = p.counts[(int64_t)blocks * n + i];
+  int held = 0;
+  if constexpr (SUM) {
+    sum_counts<64 * W>(p, blocks, table, table + n);
+  } else {
+    held = threadIdx.x < n ? mine[threadIdx.x] : 0;  // (asked for early: most calls have no more experts than threads)
+    for (int i = threadIdx.x; i < n; i += 64 * W) table[i] = p.counts[(int64_t)blocks * n + i];
+  }
   const int64_t first = blockIdx.x * chunk, last = first + chunk < p.count ? first + chunk : p.count;
   Block<W> b;
   b.count_all(p, first, last, lds);
   if (threadIdx.x < 64) {
     const int total = scan_table(table, n);
-    if (lane_id() == 0) table[n] = total;
+    if (lane_id() == 0) rows = total;
   }
   __syncthreads();
-  for (int e = threadIdx.x; e <= n; e += 64 * W) {
+  for (int e = threadIdx.x; e < n; e += 64 * W) {
     if (blockIdx.x == 0) p.offsets[e] = table[e];
-    if (e < n) start_counters<W>(lds, n, e, table[e] + (e < 64 * W ? held : mine[e]));
+    start_counters<W>(lds, n, e, table[e] + (SUM ? table[n + e] : e < 64 * W ? held : mine[e]));
   }
-  const int used = table[n];
+  const int used = rows;
+  if (blockIdx.x == 0 && threadIdx.x == 0) p.offsets[n] = used;
   __syncthreads();
   b.number_all(p);
   no_rows(p, first, last, used);
@@ -262,13 +293,17 @@ hipError_t launch_expert_sort(const SortLaunch& a, hipStream_t st) {
     return hipGetLastError();
   }
   const int64_t chunk = sort_chunk(a.count);
-  const int blocks = (int)((a.count + chunk - 1) / chunk);
+  const int blocks = (int)sort_blocks(a.count);
   sort_count_kernel<<<blocks, kCountThreads, a.n_experts * 4, st>>>(a, chunk);
+  if (sort_in_two(a.count, a.n_experts)) {
+    sort_number_kernel<16, true><<<blocks, 1024, 18 * a.n_experts * 4, st>>>(a, chunk, blocks);
+    return hipGetLastError();
+  }
   sort_scan_kernel<<<(a.n_experts + 63) / 64, 64 * kScanWaves, 0, st>>>(a, blocks);
   if (a.n_experts <= 1024)
-    sort_number_kernel<8><<<blocks, 512, (9 * a.n_experts + 1) * 4, st>>>(a, chunk, blocks);
+    sort_number_kernel<8, false><<<blocks, 512, 9 * a.n_experts * 4, st>>>(a, chunk, blocks);
   else
-    sort_number_kernel<2><<<blocks, 128, (3 * a.n_experts + 1) * 4, st>>>(a, chunk, blocks);
+    sort_number_kernel<2, false><<<blocks, 128, 3 * a.n_experts * 4, st>>>(a, chunk, blocks);
   return hipGetLastError();
 }
 

@@ -35,7 +35,8 @@ def check(e: np.ndarray, n: int):
 
 ONE = [(tokens, k, n) for tokens, k in ((1, 1), (1, 8), (8, 8), (37, 3), (64, 1), (1365, 3), (4097, 1), (4096, 2))
        for n in (1, 2, 64, 512, 513, 4096)]
-MANY = [(count, n) for count in (8193, 10007, 70001) for n in (1, 3, 65, 256, 1024, 1025, 4096)]
+MANY = [(count, n) for count in (8193, 10007, 70001) for n in (1, 3, 65, 256, 512, 513, 1024, 1025, 4096)]
+MANY += [(524288, 256), (524289, 256), (400000, 512), (360000, 512), (2 ** 21, 16), (2 ** 21 - 5, 17)]
 
 
 @pytest.mark.parametrize("tokens,k,n", ONE)
