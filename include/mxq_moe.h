@@ -44,7 +44,8 @@ mxq_status mxq_route(const void* logits, mxq_dtype dt, int64_t tokens, int64_t n
  *   dlogits[e] = sum over j with experts[j] == e of w_j dw_j, less S p_e (renorm == 0,
  *   p the softmax over all experts) or S times the weights of e (renorm == 1)
  * dlogits  [tokens, n_experts] of dt, dense (rounded once). Choices outside
- *          [0, n_experts) are left out, whatever their dw.
+ *          [0, n_experts) are left out, whatever their dw. mxq_route names an expert once for
+ *          a token; the terms of one named more often are added up in no stated order.
  * logits   as in mxq_route; not read with renorm == 1 (may be NULL). ld is then ignored.
  */
 mxq_status mxq_route_grad(const float* dw, const float* weights, const int32_t* experts, const void* logits,
