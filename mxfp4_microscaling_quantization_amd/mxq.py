@@ -333,7 +333,7 @@ def _on_gpu(first: torch.Tensor, *others: Optional[torch.Tensor]) -> int:
     if elsewhere or device != torch._C._cuda_getDevice():
         where = sorted({str(t.device) for t in (first, *others) if t is not None})
         raise ValueError(f"tensors on the current GPU expected, got some on {', '.join(where)}")
-    return _stream()
+    return torch._C._cuda_getCurrentRawStream(device)
 
 
 def _product(a, b, offsets, bias, act, residual, preact, out_dtype, out):
@@ -463,9 +463,10 @@ _ROWS = {None: 0, "mxfp4": 1, "fp8": 2}
 
 def _strided_rows(t: torch.Tensor, what: str):
     """(rows, columns, row stride) of a matrix whose columns lie side by side."""
-    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+    shape = t.shape
+    if len(shape) != 2 or (shape[1] > 1 and t.stride(1) != 1):
         raise ValueError(f"{what}: a matrix with unit column stride expected")
-    rows, cols = t.shape
+    rows, cols = shape
     # (a stride means nothing where there are fewer than two rows)
     return rows, cols, t.stride(0) if rows > 1 else cols
 
