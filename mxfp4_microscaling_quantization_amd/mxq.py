@@ -622,17 +622,21 @@ def mxq_combine_grad(grad: torch.Tensor, y: torch.Tensor, positions: torch.Tenso
     gdt, ydt = _float_code(grad.dtype), _float_code(y.dtype)
     gp, yp = _dense(grad, (tokens, width), grad.dtype, "grad"), _dense(y, (rows, width), y.dtype, "y")
     wp = None if weights is None else _dense(weights, shape, torch.float32, "weights")
+    given = []
+    if out is not None:
+        _dense(out, (rows, width), y.dtype, "out")
+        given.append(out)
+    if weight_grad and dw is not None:
+        _dense(dw, shape, torch.float32, "dw")
+        given.append(dw)
+    stream = _on_gpu(grad, y, positions, weights, *given)
     if out is None:
         out = torch.empty_like(y)
-    op = _dense(out, (rows, width), y.dtype, "out")
-    dwp = None
-    if weight_grad:
-        if dw is None:
-            dw = grad.new_empty(shape, dtype=torch.float32)
-        dwp = _dense(dw, shape, torch.float32, "dw")
-    stream = _on_gpu(grad, y, positions, weights, out, dw if weight_grad else None)
-    _check(lib().mxq_combine_grad(gp, gdt, yp, ydt, rows, width, positions.data_ptr(), wp, tokens, shape[1], op, dwp,
-                                  stream))
+    if weight_grad and dw is None:
+        dw = grad.new_empty(shape, dtype=torch.float32)
+    dwp = dw.data_ptr() if weight_grad else None
+    _check(lib().mxq_combine_grad(gp, gdt, yp, ydt, rows, width, positions.data_ptr(), wp, tokens, shape[1],
+                                  out.data_ptr(), dwp, stream))
     return (out, dw) if weight_grad else out
 
 
@@ -673,30 +677,40 @@ def mxq_fp8_act_grad(dy: torch.Tensor, z8, act: str = "none", offsets: Optional[
     dy_shape = (rows, n // 2 if code == SWIGLU else n)
     dyp = _dense(dy, dy_shape, dtype, "dy")
     groups, offp = (1, None) if offsets is None else (_offsets(offsets), offsets.data_ptr())
-    if out is None:
-        out = dy.new_empty(shape)
-    dzp = _dense(out, shape, dtype, "out")
-    got, given = [out], [out]
-    dbp = wsp = hp = None
+    given = []
+    if out is not None:
+        _dense(out, shape, dtype, "out")
+        given.append(out)
+    need = 0
     if bias_grad:
         db_shape = (n,) if offsets is None else (groups, n)
+        if db is not None:
+            _dense(db, db_shape, torch.float32, "db")
+            given.append(db)
+        need = lib().mxq_act_grad_workspace(rows, n, groups)
+        if workspace is not None:
+            if workspace.numel() * workspace.element_size() < need or not workspace.is_contiguous():
+                raise ValueError(f"dense workspace of {need} bytes expected")
+            given.append(workspace)
+    if recompute and h is not None:
+        _dense(h, dy_shape, dtype, "h")
+        given.append(h)
+    stream = _on_gpu(dy, q8, scales, offsets, *given)
+    if out is None:
+        out = dy.new_empty(shape)
+    got = [out]
+    dbp = wsp = hp = None
+    if bias_grad:
         if db is None:
             db = dy.new_empty(db_shape, dtype=torch.float32)
-        dbp = _dense(db, db_shape, torch.float32, "db")
-        need = lib().mxq_act_grad_workspace(rows, n, groups)
         if workspace is None:
             workspace = dy.new_empty((need,), dtype=torch.uint8)
-        elif workspace.numel() * workspace.element_size() < need or not workspace.is_contiguous():
-            raise ValueError(f"dense workspace of {need} bytes expected")
-        wsp = workspace.data_ptr()
+        dbp, wsp = db.data_ptr(), workspace.data_ptr()
         got.append(db)
-        given += [db, workspace]
     if recompute:
         if h is None:
             h = torch.empty_like(dy)
-        hp = _dense(h, dy_shape, dtype, "h")
+        hp = h.data_ptr()
         got.append(h)
-        given.append(h)
-    stream = _on_gpu(dy, q8, scales, offsets, *given)
-    _check(lib().mxq_fp8_act_grad(dyp, dt, qp, sp, rows, n, code, offp, groups, dzp, dbp, hp, wsp, stream))
-    return tuple(got) if len(got) > 1 else got[0]
+    _check(lib().mxq_fp8_act_grad(dyp, dt, qp, sp, rows, n, code, offp, groups, out.data_ptr(), dbp, hp, wsp, stream))
+    return tuple(got) if len(got) > 1 else out
