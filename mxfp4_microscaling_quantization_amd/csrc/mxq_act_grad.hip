@@ -36,8 +36,9 @@ __device__ __forceinline__ float act_grad_f(float dy, float z, int act) {
 // read once, so non-temporal), or rows that start on any element (the memory system takes such
 // accesses) with the last elements one by one, those past the row's end as zeros. Stores of 16 and 8
 // bytes of a lane write whole lines and go past the caches (65536 x 4096 bf16 swiglu from FP8 with h 269
-// us, through them 280); fp32's two pieces of 16, each of which writes half of every line, do not (16384
-// x 4096 fp32 141 us, past the caches 155).
+// us, through them 280), and so do rows that share lines (16384 x 4098 119 us, through them 148); fp32's
+// two pieces of 16 of whole rows, each of which writes half of every line, do not (16384 x 4096 fp32 141
+// us, past the caches 155).
 template <typename T, int V, bool VEC>
 struct Run {
   T v[V];
@@ -72,7 +73,7 @@ struct Run {
     } else if constexpr (VEC) {
       __builtin_memcpy(__builtin_assume_aligned(p, sizeof(v) < 16 ? sizeof(v) : 16), v, sizeof(v));
     } else if (left >= V) {
-      __builtin_memcpy(p, v, sizeof(v));
+      store_any<sizeof(v)>(p, v);
     } else {
 #pragma unroll
       for (int i = 0; i < V; ++i)
@@ -202,8 +203,8 @@ __global__ __launch_bounds__(256) void act_grad_kernel(ActGradLaunch p, int col_
 }
 
 // Eight rows of a wave in flight: 65536 x 4096 bf16 swiglu from FP8 with its sums and h, 1.35 GB, 269 us,
-// 5.0 TB/s (without h, 1.08 GB, 208; four rows 219). Rows that start anywhere: four (145 and 141 us of
-// 16384 x 4098).
+// 5.0 TB/s (without h, 1.08 GB, 208; four rows 219). Rows that start anywhere: four (16384 x 4098 119 us,
+// eight 123).
 template <typename T, bool SUM, bool GATED, bool VEC, bool H>
 __global__ __launch_bounds__(256) void fp8_act_grad_kernel(ActGradLaunch p, int col_tiles) {
   grad_block<T, ZRun8<VEC>, SUM, GATED, VEC, H, VEC ? 8 : 4>(p, col_tiles);

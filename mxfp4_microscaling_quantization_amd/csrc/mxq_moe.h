@@ -7,6 +7,41 @@
 
 namespace mxq {
 
+// 16 and 8 bytes anywhere: the memory system takes them from any address. Rows whose start is no multiple
+// of 16 bytes move this way, a row's last elements one by one; past the caches, as whole rows do.
+typedef nt_u32x4 any_u32x4 __attribute__((aligned(1)));
+typedef nt_u32x2 any_u32x2 __attribute__((aligned(1)));
+template <int BYTES>
+__device__ __forceinline__ void load_any(void* v, const void* p) {
+  static_assert(BYTES == 8 || BYTES % 16 == 0, "");
+  if constexpr (BYTES == 8) {
+    const nt_u32x2 x = __builtin_nontemporal_load(static_cast<const any_u32x2*>(p));
+    __builtin_memcpy(v, &x, 8);
+  } else {
+#pragma unroll
+    for (int i = 0; i < BYTES / 16; ++i) {
+      const nt_u32x4 x = __builtin_nontemporal_load(static_cast<const any_u32x4*>(p) + i);
+      __builtin_memcpy(static_cast<char*>(v) + 16 * i, &x, 16);
+    }
+  }
+}
+template <int BYTES>
+__device__ __forceinline__ void store_any(void* p, const void* v) {
+  static_assert(BYTES == 8 || BYTES % 16 == 0, "");
+  if constexpr (BYTES == 8) {
+    nt_u32x2 x;
+    __builtin_memcpy(&x, v, 8);
+    __builtin_nontemporal_store((any_u32x2)x, static_cast<any_u32x2*>(p));
+  } else {
+#pragma unroll
+    for (int i = 0; i < BYTES / 16; ++i) {
+      nt_u32x4 x;
+      __builtin_memcpy(&x, static_cast<const char*>(v) + 16 * i, 16);
+      __builtin_nontemporal_store((any_u32x4)x, static_cast<any_u32x4*>(p) + i);
+    }
+  }
+}
+
 constexpr int kHalfMirror = 0x141, kMirror = 0x140;  // lane i of 8 takes lane 7 - i, of 16 lane 15 - i
 
 // The same lane of the other 16 of 32, of the other 32 of 64.

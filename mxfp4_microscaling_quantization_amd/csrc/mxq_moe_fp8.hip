@@ -62,7 +62,7 @@ __global__ __launch_bounds__(kThreads) void fp8_rows_kernel(Fp8Params p) {
     if constexpr (VEC) {
       if (left[u] > 0) store_nt(reinterpret_cast<uint2*>(to), make_uint2(q[0], q[1]));
     } else if (left[u] >= 8) {
-      __builtin_memcpy(to, q, 8);
+      store_any<8>(to, q);
     } else {
 #pragma unroll
       for (int i = 0; i < 8; ++i)

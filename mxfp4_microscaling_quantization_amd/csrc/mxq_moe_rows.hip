@@ -17,9 +17,6 @@ __device__ __forceinline__ int row_at(const RowsLaunch& p, int64_t a) {
   return (uint32_t)r < (uint64_t)p.rows ? r : -1;
 }
 
-// 16 bytes anywhere: the memory system takes them from any address.
-typedef nt_u32x4 any_u32x4 __attribute__((aligned(2)));
-
 // Rows as they are, 16 bytes of a thread. WHOLE: rows start on 16 bytes and hold whole 16s; otherwise
 // they start anywhere, and a row's last bytes go two by two. (16384 tokens' 8 rows of 7168 bf16, 2.1 GB:
 // 395 us, 5.3 TB/s, with 256 threads 454; 2 rows of 4097 bf16, 0.4 GB: 82 us, with 128 threads 91, stores
@@ -38,7 +35,7 @@ __global__ __launch_bounds__(kCopyThreads<WHOLE>) void dispatch_copy_kernel(Rows
   if (WHOLE) {
     v = __builtin_nontemporal_load(reinterpret_cast<const nt_u32x4*>(x));
   } else if (pairs >= 8) {
-    v = __builtin_nontemporal_load(reinterpret_cast<const any_u32x4*>(x));
+    load_any<16>(&v, x);
   } else {
 #pragma unroll
     for (int i = 0; i < 7; ++i) last[i] = i < pairs ? reinterpret_cast<const uint16_t*>(x)[i] : 0;
@@ -50,7 +47,7 @@ __global__ __launch_bounds__(kCopyThreads<WHOLE>) void dispatch_copy_kernel(Rows
     if (WHOLE) {
       __builtin_nontemporal_store(v, reinterpret_cast<nt_u32x4*>(out));
     } else if (pairs >= 8) {
-      __builtin_nontemporal_store((any_u32x4)v, reinterpret_cast<any_u32x4*>(out));
+      store_any<16>(out, &v);
     } else {
 #pragma unroll
       for (int i = 0; i < 7; ++i)
@@ -134,34 +131,34 @@ __global__ __launch_bounds__(kQuantThreads) void dispatch_quantize_kernel(RowsLa
 }
 
 // Eight neighbouring elements of a row, read or written once. WHOLE: rows start on 16 bytes and hold
-// whole eights. Otherwise they start on any element (the memory system takes such accesses; 16 bytes
-// at a time all the same), and the last elements of a row go one by one.
+// whole eights; otherwise they start on any element, and the last elements of a row go one by one.
 template <typename T, bool WHOLE>
 struct Eight {
   T v[8];
   __device__ __forceinline__ void load(const T* p, int left) {
-    if (WHOLE || left >= 8) {
+    if constexpr (WHOLE) {
 #pragma unroll
       for (int i = 0; i < (int)sizeof(v) / 16; ++i) {
-        nt_u32x4 x;
-        if constexpr (WHOLE) x = __builtin_nontemporal_load(reinterpret_cast<const nt_u32x4*>(p) + i);
-        else x = __builtin_nontemporal_load(reinterpret_cast<const any_u32x4*>(p) + i);
+        const uint4 x = load_nt(reinterpret_cast<const uint4*>(p) + i);
         __builtin_memcpy(v + i * 16 / sizeof(T), &x, 16);
       }
+    } else if (left >= 8) {
+      load_any<sizeof(v)>(v, p);
     } else {
 #pragma unroll
       for (int i = 0; i < 8; ++i) v[i] = i < left ? p[i] : (T)0.0f;
     }
   }
   __device__ __forceinline__ void store(T* p, int left) const {
-    if (WHOLE || left >= 8) {
+    if constexpr (WHOLE) {
 #pragma unroll
       for (int i = 0; i < (int)sizeof(v) / 16; ++i) {
-        nt_u32x4 x;
+        uint4 x;
         __builtin_memcpy(&x, v + i * 16 / sizeof(T), 16);
-        if constexpr (WHOLE) __builtin_nontemporal_store(x, reinterpret_cast<nt_u32x4*>(p) + i);
-        else __builtin_nontemporal_store((any_u32x4)x, reinterpret_cast<any_u32x4*>(p) + i);
+        store_nt(reinterpret_cast<uint4*>(p) + i, x);
       }
+    } else if (left >= 8) {
+      store_any<sizeof(v)>(p, v);
     } else {
 #pragma unroll
       for (int i = 0; i < 8; ++i)
