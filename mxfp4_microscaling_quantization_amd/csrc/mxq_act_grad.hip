@@ -7,7 +7,6 @@ namespace mxq {
 
 namespace {
 
-constexpr int kCols = 512;  // columns of a workgroup: 64 lanes of 8
 
 // act'(z) and, for SWIGLU, both halves of a pair (gate g, up u). Far from zero s is 0 or 1 exactly
 // (for gelu from |z| = 11 on, for silu's from 89 on) and so is the slope: the polynomials that s
@@ -37,8 +36,7 @@ __device__ __forceinline__ float act_grad_f(float dy, float z, int act) {
 // accesses) with the last elements one by one, those past the row's end as zeros. Stores of 16 and 8
 // bytes of a lane write whole lines and go past the caches (65536 x 4096 bf16 swiglu from FP8 with h 269
 // us, through them 280), and so do rows that share lines (16384 x 4098 119 us, through them 148); fp32's
-// two pieces of 16 of whole rows, each of which writes half of every line, do not (16384 x 4096 fp32 141
-// us, past the caches 155).
+// two pieces of 16 of whole rows, each of which writes half of every line, do not.
 template <typename T, int V, bool VEC>
 struct Run {
   T v[V];
@@ -82,50 +80,54 @@ struct Run {
   }
 };
 
-// Eight neighbouring values of z: as they are, or E4M3 under the scale of their 128 columns.
-template <typename T, bool VEC>
+// V neighbouring values of z: as they are, or E4M3 under the scale of their 128 columns.
+template <typename T, int V, bool VEC>
 struct ZRun {
-  Run<T, 8, VEC> run;
+  Run<T, V, VEC> run;
   __device__ __forceinline__ void load(const ActGradLaunch& p, int64_t row, int64_t col, int64_t left) {
     run.load(static_cast<const T*>(p.z) + row * p.n + col, left);
   }
-  __device__ __forceinline__ void values(float (&v)[8]) const {
+  __device__ __forceinline__ void values(float (&v)[V]) const {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = (float)run.v[i];
+    for (int i = 0; i < V; ++i) v[i] = (float)run.v[i];
   }
 };
-template <bool VEC>
+template <int V, bool VEC>
 struct ZRun8 {
-  uint2 q;
-  uint32_t scale;
+  uint32_t q[V / 4], scale;
   __device__ __forceinline__ void load(const ActGradLaunch& p, int64_t row, int64_t col, int64_t left) {
     const uint8_t* z = static_cast<const uint8_t*>(p.z) + row * p.n + col;
     scale = as_u(p.z_scales[row * ((p.n + 127) / 128) + col / 128]);
-    if constexpr (VEC) {
-      q = load_nt(reinterpret_cast<const uint2*>(z));
-    } else if (left >= 8) {
-      __builtin_memcpy(&q, z, 8);
+    if constexpr (VEC && V == 8) {
+      const uint2 x = load_nt(reinterpret_cast<const uint2*>(z));
+      __builtin_memcpy(q, &x, 8);
+    } else if constexpr (VEC) {
+      q[0] = load_nt(reinterpret_cast<const uint32_t*>(z));
+    } else if (left >= V) {
+      __builtin_memcpy(q, z, V);
     } else {
-      uint8_t b[8];
+      uint8_t b[V];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) b[i] = i < left ? z[i] : 0;
-      __builtin_memcpy(&q, b, 8);
+      for (int i = 0; i < V; ++i) b[i] = i < left ? z[i] : 0;
+      __builtin_memcpy(q, b, V);
     }
   }
-  __device__ __forceinline__ void values(float (&v)[8]) const {
+  __device__ __forceinline__ void values(float (&v)[V]) const {
     const float s = fp8_scale(scale);
-    const f32x2_t a = __builtin_amdgcn_cvt_pk_f32_fp8((int)q.x, false), b = __builtin_amdgcn_cvt_pk_f32_fp8((int)q.x, true);
-    const f32x2_t c = __builtin_amdgcn_cvt_pk_f32_fp8((int)q.y, false), d = __builtin_amdgcn_cvt_pk_f32_fp8((int)q.y, true);
-    v[0] = a.x * s; v[1] = a.y * s; v[2] = b.x * s; v[3] = b.y * s;
-    v[4] = c.x * s; v[5] = c.y * s; v[6] = d.x * s; v[7] = d.y * s;
+#pragma unroll
+    for (int i = 0; i < V / 4; ++i) {
+      const f32x2_t a = __builtin_amdgcn_cvt_pk_f32_fp8((int)q[i], false), b = __builtin_amdgcn_cvt_pk_f32_fp8((int)q[i], true);
+      v[4 * i] = a.x * s; v[4 * i + 1] = a.y * s; v[4 * i + 2] = b.x * s; v[4 * i + 3] = b.y * s;
+    }
   }
 };
 
-// One workgroup: up to p.block_rows rows of one group, 512 columns. Its waves take every
+// One workgroup: up to p.block_rows rows of one group, V columns of a lane. Its waves take every
 // fourth row, four of them in flight: their loads go ahead of the first one's arithmetic.
 // The sums of the four waves are added in order through LDS. H: act(z) goes out as well.
-template <typename T, typename Z, bool SUM, bool GATED, bool VEC, bool H, int U>
+template <typename T, typename Z, int V, bool SUM, bool GATED, bool VEC, bool H, int U>
 __device__ __forceinline__ void grad_block(const ActGradLaunch& p, int col_tiles) {
+  constexpr int kCols = 64 * V, D = GATED ? V / 2 : V;  // D: a lane's values of dy
   __shared__ float sums[4][kCols];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int block = blockIdx.x / col_tiles, col_tile = blockIdx.x % col_tiles;
@@ -133,8 +135,8 @@ __device__ __forceinline__ void grad_block(const ActGradLaunch& p, int col_tiles
   if (p.offsets && !find_segment(p.offsets, p.groups, p.rows, p.block_rows, block, s)) return;
   const int64_t first = (int64_t)s.tile * p.block_rows;
   const int count = (int)(s.count - first < p.block_rows ? s.count - first : p.block_rows);
-  const int64_t col = (int64_t)col_tile * kCols + lane * 8, left = p.n - col;
-  float sum[8] = {};
+  const int64_t col = (int64_t)col_tile * kCols + lane * V, left = p.n - col;
+  float sum[V] = {};
   if (left > 0) {
     const int64_t dn = GATED ? p.n / 2 : p.n;
     const int64_t from = (s.begin + first) * dn + (GATED ? col / 2 : col);
@@ -143,7 +145,7 @@ __device__ __forceinline__ void grad_block(const ActGradLaunch& p, int col_tiles
     T* h = H ? static_cast<T*>(p.h) + from : nullptr;
     for (int r0 = wave; r0 < count; r0 += 4 * U) {
       Z zr[U];
-      Run<T, GATED ? 4 : 8, VEC> dr[U];
+      Run<T, D, VEC> dr[U];
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         const int64_t row = r0 + 4 * u < count ? r0 + 4 * u : count - 1;
@@ -153,12 +155,12 @@ __device__ __forceinline__ void grad_block(const ActGradLaunch& p, int col_tiles
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         if (r0 + 4 * u >= count) break;
-        float z[8], v[8];
-        Run<T, GATED ? 4 : 8, VEC> ho;
+        float z[V], v[V];
+        Run<T, D, VEC> ho;
         zr[u].values(z);
         if constexpr (GATED) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
+          for (int i = 0; i < D; ++i) {
             const float g = z[2 * i], up = z[2 * i + 1], d = (float)dr[u].v[i];
             const float sg = sigmoid_f(g);
             v[2 * i] = d * up * silu_slope(g, sg);
@@ -167,15 +169,15 @@ __device__ __forceinline__ void grad_block(const ActGradLaunch& p, int col_tiles
           }
         } else {
 #pragma unroll
-          for (int i = 0; i < 8; ++i) v[i] = act_grad_f((float)dr[u].v[i], z[i], p.act);
+          for (int i = 0; i < V; ++i) v[i] = act_grad_f((float)dr[u].v[i], z[i], p.act);
           if constexpr (H) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) ho.v[i] = (T)act_f(z[i], p.act);
+            for (int i = 0; i < V; ++i) ho.v[i] = (T)act_f(z[i], p.act);
           }
         }
-        Run<T, 8, VEC> o;
+        Run<T, V, VEC> o;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
+        for (int i = 0; i < V; ++i) {
           if (SUM) sum[i] += v[i];
           o.v[i] = (T)v[i];
         }
@@ -186,7 +188,7 @@ __device__ __forceinline__ void grad_block(const ActGradLaunch& p, int col_tiles
   }
   if constexpr (SUM) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) sums[wave][lane * 8 + i] = sum[i];
+    for (int i = 0; i < V; ++i) sums[wave][lane * V + i] = sum[i];
     __syncthreads();
     for (int c = threadIdx.x; c < kCols; c += 256) {
       const int64_t at = (int64_t)col_tile * kCols + c;
@@ -199,15 +201,18 @@ __device__ __forceinline__ void grad_block(const ActGradLaunch& p, int col_tiles
 // plain stream that reads twice what it writes reaches here.
 template <typename T, bool SUM, bool GATED, bool VEC>
 __global__ __launch_bounds__(256) void act_grad_kernel(ActGradLaunch p, int col_tiles) {
-  grad_block<T, ZRun<T, VEC>, SUM, GATED, VEC, false, 4>(p, col_tiles);
+  grad_block<T, ZRun<T, 8, VEC>, 8, SUM, GATED, VEC, false, 4>(p, col_tiles);
 }
 
 // Eight rows of a wave in flight: 65536 x 4096 bf16 swiglu from FP8 with its sums and h, 1.35 GB, 269 us,
 // 5.0 TB/s (without h, 1.08 GB, 208; four rows 219). Rows that start anywhere: four (16384 x 4098 119 us,
 // eight 123).
+// 16 bytes of a lane's dz: 8 columns in bf16, 4 in fp32 (16384 x 4096 fp32 with h 132 us, 8 columns 150).
+template <typename T>
+constexpr int kFp8Run = 16 / sizeof(T);
 template <typename T, bool SUM, bool GATED, bool VEC, bool H>
 __global__ __launch_bounds__(256) void fp8_act_grad_kernel(ActGradLaunch p, int col_tiles) {
-  grad_block<T, ZRun8<VEC>, SUM, GATED, VEC, H, VEC ? 8 : 4>(p, col_tiles);
+  grad_block<T, ZRun8<kFp8Run<T>, VEC>, kFp8Run<T>, SUM, GATED, VEC, H, VEC ? 8 : 4>(p, col_tiles);
 }
 
 // db[g] = the partial sums of the group's row blocks. A column has kLanes threads, each with
@@ -250,6 +255,7 @@ __global__ __launch_bounds__(64 * kLanes) void act_grad_sum_kernel(ActGradLaunch
 
 template <typename T, bool SUM, bool GATED>
 struct Rows {
+  static constexpr int kRun = 8;
   static void launch(const ActGradLaunch& a, dim3 grid, int col_tiles, hipStream_t st) {
     if (a.n % 8 == 0)
       act_grad_kernel<T, SUM, GATED, true><<<grid, 256, 0, st>>>(a, col_tiles);
@@ -259,6 +265,7 @@ struct Rows {
 };
 template <typename T, bool SUM, bool GATED>
 struct Fp8Rows {
+  static constexpr int kRun = kFp8Run<T>;
   template <bool VEC>
   static void launch_v(const ActGradLaunch& a, dim3 grid, int col_tiles, hipStream_t st) {
     if (a.h)
@@ -274,6 +281,7 @@ struct Fp8Rows {
 
 template <template <typename, bool, bool> class Kernel, typename T>
 hipError_t launch_t(ActGradLaunch a, hipStream_t st) {
+  constexpr int kCols = 64 * Kernel<T, true, true>::kRun;
   const int64_t col_tiles = (a.n + kCols - 1) / kCols, blocks = act_grad_blocks(a.rows, a.groups, a.block_rows);
   // one block of rows: its sums are the bias gradient
   const bool direct = a.db && !a.offsets && blocks == 1;

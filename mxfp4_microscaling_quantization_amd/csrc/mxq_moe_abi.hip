@@ -205,8 +205,9 @@ mxq_status mxq_fp8_act_grad(const void* dy, mxq_dtype dt, const uint8_t* z8, con
   if (rows > 0 && (!dy || !z8 || !z_scales || !dz || (db && !workspace))) return MXQ_EINVAL;
   if (n == 0 || n > kMaxDim || rows > kMaxDim || rows > ((int64_t)1 << 40) / n) return MXQ_ESHAPE;
   if (act == MXQ_ACT_SWIGLU && n % 2) return MXQ_ESHAPE;
-  // the grids enumerate row blocks x column tiles and groups x column tiles
-  if (act_grad_blocks(rows, n_experts, act_grad_rows(rows, n)) * ((n + 511) / 512) >= kMaxGrid / 64 ||
+  // the grids enumerate row blocks x column tiles (16 bytes of 64 lanes) and groups x column tiles
+  const int64_t tile = 64 * 16 / size_of(dt);
+  if (act_grad_blocks(rows, n_experts, act_grad_rows(rows, n)) * ((n + tile - 1) / tile) >= kMaxGrid / 64 ||
       n_experts * ((n + 63) / 64) >= kMaxGrid / 256)
     return MXQ_ESHAPE;
   if (!aligned(dy, 16) || !aligned(z8, 16) || !aligned(z_scales, 4) || !aligned(dz, 16) || !aligned(db, 16) ||

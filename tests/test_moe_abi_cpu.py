@@ -155,6 +155,7 @@ FP8_GRAD = dict(dy=FAKE, dt=0, z8=FAKE, scales=FAKE, rows=4, n=8, act=1, off=Non
     (dict(db=FAKE), EINVAL), (dict(dt=2), EINVAL), (dict(act=5), EINVAL), (dict(act=-1), EINVAL), (dict(rows=-1), EINVAL),
     (dict(n=-1), EINVAL), (dict(E=2), EINVAL), (dict(off=FAKE, E=0), EINVAL), (dict(off=FAKE, E=4097), EINVAL),
     (dict(n=0), ESHAPE), (dict(act=4, n=7), ESHAPE), (dict(n=2 ** 31), ESHAPE), (dict(rows=2 ** 21, n=2 ** 20), ESHAPE),
+    (dict(dt=1, rows=2 ** 30 + 2 ** 14, n=512), ESHAPE), (dict(rows=2 ** 30 + 2 ** 14, n=1024), ESHAPE),
     (dict(dy=FAKE + 8), EALIGN), (dict(z8=FAKE + 8), EALIGN), (dict(scales=FAKE + 2), EALIGN), (dict(dz=FAKE + 2), EALIGN),
     (dict(h=FAKE + 8), EALIGN), (dict(db=FAKE + 4, ws=FAKE), EALIGN), (dict(db=FAKE, ws=FAKE + 8), EALIGN),
     (dict(off=FAKE + 4), EALIGN), (dict(rows=0, dy=None, z8=None, dz=None), OK),

@@ -78,6 +78,8 @@ def test_largest_sizes_stay_within_a_launch(tmp_path):
            of("mxq_dispatch", BASE, 1, 2 ** 16, 2 ** 22, 2 ** 22, BASE, 2, 2 ** 17, 2, BASE, BASE),
            of("mxq_combine", BASE, 0, 2 ** 18, 2 ** 22 - 1, BASE, None, 2 ** 16, 64, None, BASE, 1),
            of("mxq_combine_grad", BASE, 0, BASE, 0, 2 ** 18, 2 ** 22, BASE, None, 2 ** 16, 64, BASE, BASE),
+           of("mxq_fp8_act_grad", BASE, 1, BASE, BASE, 2 ** 30 - 2 ** 13, 512, 3, None, 1, BASE, BASE, BASE, BASE),
+           of("mxq_fp8_act_grad", BASE, 0, BASE, BASE, 2 ** 31 - 2 ** 13, 512, 3, None, 1, BASE, None, BASE, BASE),
            of("mxq_fp8_quantize", BASE, 1, 2 ** 10, 2 ** 30 - 1, 2 ** 30 - 1, BASE, BASE)]
     for call, (status, launches, _) in zip(big, record(big, tmp_path)):
         assert status == mxq.MXQ_OK and launches, call
