@@ -5,7 +5,7 @@
  * Pointers, streams, ownership, status codes and byte layouts are those of mxq.h.
  *
  * T tokens choose k experts each; assignment t k + j is token t's choice j. Its row among
- * the rows of all experts is positions[t, k + j]; a position outside [0, rows) (-1, as
+ * the rows of all experts is positions[t, j]; a position outside [0, rows) (-1, as
  * mxq_expert_sort writes it) stands for an assignment without a row, which reads and
  * writes nothing. Two assignments must not have the same row.
  *

@@ -7,7 +7,6 @@ namespace mxq {
 
 namespace {
 
-
 // act'(z) and, for SWIGLU, both halves of a pair (gate g, up u). Far from zero s is 0 or 1 exactly
 // (for gelu from |z| = 11 on, for silu's from 89 on) and so is the slope: the polynomials that s
 // (1 - s) holds down there take z clamped, or they would be infinite and their products with
@@ -123,7 +122,7 @@ struct ZRun8 {
 };
 
 // One workgroup: up to p.block_rows rows of one group, V columns of a lane. Its waves take every
-// fourth row, four of them in flight: their loads go ahead of the first one's arithmetic.
+// fourth row, U of them in flight: their loads go ahead of the first one's arithmetic.
 // The sums of the four waves are added in order through LDS. H: act(z) goes out as well.
 template <typename T, typename Z, int V, bool SUM, bool GATED, bool VEC, bool H, int U>
 __device__ __forceinline__ void grad_block(const ActGradLaunch& p, int col_tiles) {
@@ -206,8 +205,8 @@ __global__ __launch_bounds__(256) void act_grad_kernel(ActGradLaunch p, int col_
 
 // Eight rows of a wave in flight: 65536 x 4096 bf16 swiglu from FP8 with its sums and h, 1.35 GB, 269 us,
 // 5.0 TB/s (without h, 1.08 GB, 208; four rows 219). Rows that start anywhere: four (16384 x 4098 119 us,
-// eight 123).
-// 16 bytes of a lane's dz: 8 columns in bf16, 4 in fp32 (16384 x 4096 fp32 with h 132 us, 8 columns 150).
+// eight 123). 16 bytes of a lane's dz: 8 columns in bf16, 4 in fp32 (16384 x 4096 fp32 with h 132 us, 8
+// columns 150).
 template <typename T>
 constexpr int kFp8Run = 16 / sizeof(T);
 template <typename T, bool SUM, bool GATED, bool VEC, bool H>

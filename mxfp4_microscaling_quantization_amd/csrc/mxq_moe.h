@@ -1,5 +1,5 @@
-// Device-side building blocks of the operators around the experts' products: reductions
-// over groups of lanes and exponentials.
+// Device-side building blocks of the operators around the experts' products: accesses at any
+// address, reductions over groups of lanes and exponentials.
 #pragma once
 
 #include "mxq_device.h"

@@ -10,6 +10,7 @@ from tests.gpu_helpers import bits32, require_gpu, u8
 from tests.mm_helpers import U, act_bound, close, f64, out_bound
 from tests.moe_helpers import to
 from tests.test_gpu_act_grad import slope_bound
+from tests.test_gpu_mm_malformed import PATTERNS, banded, offsets
 
 pytestmark = pytest.mark.gpu
 
@@ -139,6 +140,27 @@ def test_no_rows():
     dy = torch.empty((0, 24), device="cuda:0")
     dz, db, h = mxq.mxq_fp8_act_grad(dy, z8, "relu", bias_grad=True, recompute=True)
     assert dz.shape == h.shape == (0, 24) and torch.equal(db, torch.zeros(24, device="cuda:0"))
+
+
+@pytest.mark.parametrize("kind", PATTERNS)
+@pytest.mark.parametrize("groups", [5, 130])
+@pytest.mark.parametrize("m", [40, 700])
+def test_malformed_offsets(m, groups, kind):
+    """Results are unspecified, but nothing outside the buffers is read into a sum or written."""
+    require_gpu()
+    n = 136
+    z8 = mxq.mxq_fp8_quantize(torch.ones(m, n, device="cuda:0"))
+    (dz, dz_ok), (h, h_ok) = banded((m, n), torch.float32), banded((m, n), torch.float32)
+    db, db_ok = banded((groups, n), torch.float32)
+    need = mxq.lib().mxq_act_grad_workspace(m, n, groups)
+    ws = torch.full((need // 4 + 2 * 65536,), float("nan"), device="cuda:0")
+    inner = ws[65536:65536 + need // 4]
+    inner.zero_()
+    mxq.mxq_fp8_act_grad(torch.ones(m, n, device="cuda:0"), z8, "relu", offsets(kind, m, groups), bias_grad=True,
+                         recompute=True, out=dz, db=db, h=h, workspace=inner.view(torch.uint8))
+    assert dz_ok() and db_ok() and h_ok()
+    assert torch.isnan(ws[:65536]).all() and torch.isnan(ws[65536 + need // 4:]).all()
+    assert torch.isfinite(db).all() and db.min() >= 0 and db.max() <= m
 
 
 def test_against_differences():
