@@ -35,7 +35,9 @@ __device__ __forceinline__ float act_grad_f(float dy, float z, int act) {
 // accesses) with the last elements one by one, those past the row's end as zeros. Stores of 16 and 8
 // bytes of a lane write whole lines and go past the caches (65536 x 4096 bf16 swiglu from FP8 with h 269
 // us, through them 280), and so do rows that share lines (16384 x 4098 119 us, through them 148); fp32's
-// two pieces of 16 of whole rows, each of which writes half of every line, do not.
+// two pieces of 16 of whole rows, each of which writes half of every line, do not (mxq_act_grad, us through the
+// caches and past them: 16384 x 4096 silu 192 and 228, 65536 x 4096 gelu 650 and 851, swiglu with sums 555 and
+// 624, 4096 x 4096 gelu 42.0 and 46.1).
 template <typename T, int V, bool VEC>
 struct Run {
   T v[V];
@@ -221,10 +223,13 @@ __global__ __launch_bounds__(256) void act_grad_kernel(ActGradLaunch p, int col_
   grad_block<T, ZRun<T, 8, VEC>, 8, SUM, GATED, VEC, false, 4>(p, col_tiles);
 }
 
-// Eight rows of a wave in flight: 65536 x 4096 bf16 swiglu from FP8 with its sums and h, 1.35 GB, 269 us,
-// 5.0 TB/s (without h, 1.08 GB, 208; four rows 219). Rows that start anywhere: four (16384 x 4098 119 us,
-// eight 123). 16 bytes of a lane's dz: 8 columns in bf16, 4 in fp32 (16384 x 4096 fp32 with h 132 us, 8
-// columns 150).
+// Eight rows of a wave in flight: 65536 x 4096 bf16 swiglu from FP8, 64 experts, with its sums and h, 1.35
+// GB, 269 us, 5.0 TB/s, with four 278 (without h, 1.08 GB, 205 and 213; fp32 with h 450 and 467). Blocks of 16
+// rows, which act_grad_rows gives smaller matrices, have but four for a wave: the other loads are of its last
+// row again, for nothing, and four in flight would take less there (4096 x 4096 bf16 with h 27.8 us, four 24.3;
+// 16384 x 1024 27.8 and 24.3, fp32 38.5 and 34.9; 4096 x 14336 gelu without h 77.9 and 63.7). Rows that start
+// anywhere: four (16384 x 4098 119 us, eight 123). 16 bytes of a lane's dz: 8 columns in bf16, 4 in fp32 (16384 x
+// 4096 fp32 with h 132 us, 8 columns 150).
 template <typename T>
 constexpr int kFp8Run = 16 / sizeof(T);
 template <typename T, bool SUM, bool GATED, bool VEC, bool H>

@@ -39,8 +39,14 @@ struct SortLaunch {
   int32_t *positions, *order;
   int32_t* counts;  // workspace [blocks, n_experts], then [n_experts]
 };
-// Up to this many assignments one workgroup does everything in one launch (256 experts, us: 4096
-// assignments 6.6, 6144 8.5 and 11.4 in three launches, 8192 10.0 and 11.4, 12288 13.4 and 11.4).
+// Up to this many assignments one workgroup does everything in one launch, without a workspace. (One
+// launch and the two or, past 512 experts, three that would do it otherwise, us of calls in a row. 64 experts:
+// 4096 assignments 5.4 and 7.5, 6144 7.1 and 7.4, 8192 8.4 and 7.6, 12288 11.2 and 7.7. 256: 6.1 and 7.9, 8.1 and
+// 8.2, 9.5 and 8.2, 13.0 and 8.6. 512: 6.9 and 8.8, 9.0 and 9.0, 10.5 and 9.2, 14.2 and 9.6. 1024, where the
+// workgroup has two waves instead of 16: 1024 assignments 10.4 and 12.1, 2048 16.1 and 13.7, 8192 50.3 and 13.7.
+// So between 6144 and the limit a call of up to 512 experts takes up to 1.3 us more than it need, and one of
+// more experts loses from between 1024 and 2048 on. The limit is older than the two launches; callers may give no
+// workspace up to it.)
 constexpr int64_t kSortOne = 8192;
 // Assignments of a block otherwise: as many as keep the table of counts at 1024 blocks at most.
 constexpr int64_t sort_chunk(int64_t count) {
@@ -48,9 +54,11 @@ constexpr int64_t sort_chunk(int64_t count) {
 }
 constexpr int64_t sort_blocks(int64_t count) { return (count + sort_chunk(count) - 1) / sort_chunk(count); }
 // Two launches, every block summing up the table of counts for itself, while all of them together read
-// up to 64 MiB of it; else three. (Two and three launches, us of the kernels: 33600 assignments to 256
-// experts 10.2 and 11.6, 131072 10.1 and 12.0, 524288 14.5 and 13.8, but with the launches' own time
-// 14.7 and 16.6; 524288 to 64 experts 10.7 and 12.2, to 512 19.5 and 15.1.)
+// up to 64 MiB of it; else three. (Two and three launches, us of calls in a row from C. 256 experts: 131072
+// assignments 9.6 and 11.4, 262144 11.1 and 11.9, 524288, the last size of two, 14.5 and 13.6, 655360 22.2 and
+// 18.1, 1048576 28.3 and 21.1. 64: 524288 10.1 and 12.0, 1048576, the last, 16.8 and 18.0, 2097152 31.3 and
+// 27.8. 512: 131072 11.2 and 12.4, 262144 13.9 and 13.1, and past the last size 524288 20.4 and 15.1. Through the
+// Python binding, where the host's time for a third launch counts, 524288 to 256 experts 14.1 and 17.2.)
 constexpr bool sort_in_two(int64_t count, int64_t experts) {
   return experts <= 512 && sort_blocks(count) * sort_blocks(count) * experts <= (int64_t)1 << 24;
 }

@@ -6,9 +6,10 @@
 // wave), so what counts is instructions: every lane keeps its four largest logits in order,
 // the k rounds look at the first of each lane only, and the wave goes through all logits again
 // only when a lane has given away its four. 65536 tokens of 256 bf16 logits, 8 chosen, half of
-// the experts masked: 12.7 us with 350 instructions for four tokens (264 and 12 for each choice,
-// about); looking through all logits in every round 20.6 with 616. The gradient there (67 MB): 17 us,
-// 4 TB/s.
+// the experts masked: 11.4 us of calls in a row (12.7 in a kernel trace) with 350 instructions for four
+// tokens (264 and 12 for each choice, about); looking through all logits in every round 20.6 with 616. The
+// same, none masked, fp32: 24.2 us (32768 tokens 14.9); with the softmax over all experts bf16 15.5, fp32 28.8. The
+// gradient there in bf16: over all experts (67 MB) 16.1 us, 4 TB/s, over the chosen (40 MB) 9.6.
 #include "mxq_moe.h"
 
 namespace mxq {
@@ -371,8 +372,8 @@ hipError_t launch_g(const RouteLaunch& all, bool grad, hipStream_t st) {
 }
 
 // Lanes of a token: few leave more logits to a lane, which then more often gives away its four; many
-// take more steps to compare the lanes. (65536 tokens of 256 bf16 logits: 8 lanes 14.6 us, 16 13.1, 32
-// 18.7; 32768 of fp32: 30.5, 15.6 and 15.2.)
+// take more steps to compare the lanes. (65536 tokens of 256 bf16 logits: 8 lanes 12.8 us, 16 11.6, 32
+// 16.3; 32768 of fp32: 28.9, 15.2 and 14.4.)
 template <typename T>
 hipError_t launch_t(const RouteLaunch& a, bool grad, hipStream_t st) {
   if (a.experts <= 64) return launch_g<T, 8, 8>(a, grad, st);

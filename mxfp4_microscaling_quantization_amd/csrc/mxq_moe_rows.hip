@@ -20,7 +20,8 @@ __device__ __forceinline__ int row_at(const RowsLaunch& p, int64_t a) {
 // Rows as they are, 16 bytes of a thread. WHOLE: rows start on 16 bytes and hold whole 16s; otherwise
 // they start anywhere, and a row's last bytes go two by two. (16384 tokens' 8 rows of 7168 bf16, 2.1 GB:
 // 395 us, 5.3 TB/s, with 256 threads 454; 2 rows of 4097 bf16, 0.4 GB: 82 us, with 128 threads 91, stores
-// through the caches 87, element by element 146.)
+// through the caches 87, element by element 146.) A row of less than 2 KiB leaves threads without work:
+// 65536 tokens' 4 rows of 128 bf16 39.6 us, 2.1 TB/s, of 256 50.2 and 3.3, of 512 65.3 and 5.1.
 template <bool WHOLE>
 constexpr int kCopyThreads = WHOLE ? 128 : 256;
 template <bool WHOLE>
@@ -284,7 +285,8 @@ __global__ __launch_bounds__(kGradThreads) void combine_grad_kernel(RowsLaunch p
 
 // The rows' gradients alone: a part of a token's columns, weighted for each of its assignments. (14368
 // tokens, 5 rows of 2200 bf16 from fp32, 0.44 GB: 99 us; parts of 512 columns 106, of 2048 120, a token in
-// a workgroup 115.)
+// a workgroup 115. Narrow rows leave threads without work: 65536 tokens, 4 rows of 128 bf16 from fp32, 59.5 us, 1.7
+// TB/s, of 256 71.0 and 2.8, of 512 87.3 and 4.6.)
 constexpr int kWeightThreads = 128;
 template <typename G, typename Y, bool WHOLE>
 __global__ __launch_bounds__(kWeightThreads) void combine_grad_rows_kernel(RowsLaunch p, int tiles) {
@@ -332,7 +334,10 @@ hipError_t launch_copy(const RowsLaunch& all, int64_t ld, int64_t bytes, hipStre
 template <typename T, bool FP8>
 hipError_t launch_quantize(const RowsLaunch& all, hipStream_t st) {
   const int64_t waves = (all.width / (FP8 ? 16 : 32) + 63) / 64;
-  // few tokens: a wave for each part
+  // Few tokens: a wave for each part, so that one token's parts run side by side. (us, such waves and a whole
+  // token in a workgroup, 8 rows of 7168 bf16: FP8 64 tokens 3.9 and 5.8, 256 5.0 and 6.3, 512 7.5 and 7.8, 1024
+  // 14.8 and 13.9, 1500 20.2 and 19.4; MXFP4 64 tokens 3.7 and 4.0, 512 5.4 and 5.1, 1024 9.2 and 8.8, 4096 31.6
+  // and 29.4. Rows of 2048: alike up to 512, FP8 1024 5.3 and 5.0.)
   const bool few = all.tokens < 1024;
   const int threads = few ? 64 : 64 * (int)(waves < kQuantThreads / 64 ? waves : kQuantThreads / 64);
   const int tiles = few ? (int)waves : 1;

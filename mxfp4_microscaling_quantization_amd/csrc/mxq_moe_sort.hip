@@ -12,8 +12,12 @@
 // number of such lanes below itself, and the last of them moves the counter on. No order
 // depends on timing: the only atomics add whole numbers.
 //
-// Bound by latency: 524288 assignments to 256 experts move 6.3 MB and take 14.5 us, 3.5 of them the
-// counting (three launches with a quarter of the loads in flight and half of the waves took 23).
+// 524288 assignments to 256 experts move 6.3 MB and take 14.1 us, in a kernel trace 3.5 the counting and 11.6
+// the numbering (three launches with a quarter of the loads in flight and half of the waves took 23). What
+// the numbering does first is wait: each of its 256 workgroups reads the whole table, 64 MiB of L2 reads in
+// all, 64 loads of a thread in four batches, and then, behind a barrier, its assignments, of which two of a
+// lane's four turns are empty. To 4096 experts it takes 56 us, 47 of them numbering with two waves of a
+// workgroup for 4096 counters each.
 #include "mxq_moe.h"
 
 namespace mxq {
